@@ -12,6 +12,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,13 +20,13 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdfssm.so")
 VARIANTS = {"": ([], LIB), "phases": (["-DDFSSM_PHASE_TIMERS"], os.path.join(PKG, "libdfssm_phases.so"))}
-SOURCES = ["dfssm_api.cu"]
+SOURCES = ["dfssm_api.cu", "mixer_api.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC,-fvisibility=hidden",
-    "-shared", "-cudart", "static",
+    "-cudart", "static",
     "--expt-relaxed-constexpr",
 ]
 
@@ -48,12 +49,19 @@ def build(force: bool = False, verbose: bool = False, variant: str = "") -> str:
     defines, lib = VARIANTS[variant]
     if not force and up_to_date(lib):
         return lib
-    cmd = [NVCC, *FLAGS, *defines, "-I", INCLUDE, "-I", CSRC, "-o", lib + ".tmp",
-           *[os.path.join(CSRC, s) for s in SOURCES]]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory(prefix="dfssm_build_") as tmp:
+        objs = [os.path.join(tmp, src + ".o") for src in SOURCES]
+        cmds = [[NVCC, *(["-Xptxas=-v"] if verbose else []), *FLAGS, *defines, "-I", INCLUDE, "-I", CSRC, "-c",
+                 os.path.join(CSRC, src), "-o", obj] for src, obj in zip(SOURCES, objs)]
+        procs = []
+        for cmd in cmds:                      # the sources compile side by side
+            if verbose:
+                print(" ".join(cmd))
+            procs.append(subprocess.Popen(cmd))
+        for cmd, code in zip(cmds, [p.wait() for p in procs]):
+            if code:
+                raise subprocess.CalledProcessError(code, cmd)
+        subprocess.run([NVCC, *FLAGS, "-shared", "-o", lib + ".tmp", *objs], check=True)
     os.replace(lib + ".tmp", lib)
     return lib
 

@@ -1,7 +1,5 @@
 // C ABI of libdfssm.so: host-side argument validation, workspace layout and the
 // launch sequences of the DF-SSM decode step.  Declarations and semantics: dfssm.h.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <array>
 #include <cstdarg>
@@ -13,88 +11,13 @@
 #include <vector>
 
 #include "dfssm.h"
+#include "host.cuh"
 #include "kernels.cuh"
 #include "persistent.cuh"
 
 using namespace dfssm;
 
 namespace {
-
-thread_local std::string g_last_error;
-
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return code;
-}
-
-int ok() {
-  g_last_error.clear();
-  return DFSSM_OK;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-#define REQUIRE(cond, code, ...) \
-  do {                           \
-    if (!(cond)) return fail(code, __VA_ARGS__); \
-  } while (0)
-
-#define REQUIRE_PTR(p) \
-  do { \
-    REQUIRE((p) != nullptr, DFSSM_ERR_INVALID_ARG, "%s is NULL", #p); \
-    REQUIRE(aligned16(p), DFSSM_ERR_MISALIGNED, "%s is not 16-byte aligned", #p); \
-  } while (0)
-
-#define CHECK_LAUNCH(what) \
-  do { \
-    cudaError_t e_ = cudaGetLastError(); \
-    if (e_ != cudaSuccess) return fail(DFSSM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e_)); \
-  } while (0)
-
-// Kernels of the multi-launch chain are launched with programmatic stream
-// serialization: each may start while the kernel before it still runs, does its setup
-// and reads only weights until pdl_wait() (common.cuh), so the launch and the setup
-// overlap the previous kernel's tail.  DFSSM_PDL=0 at compile time turns it off.
-#ifndef DFSSM_PDL
-#define DFSSM_PDL 1
-#endif
-template <typename... KArgs, typename... Args>
-cudaError_t launch_chain(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                         unsigned cluster_z, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[2];
-  unsigned n = 0;
-  if (DFSSM_PDL) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  if (cluster_z > 0) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n].val.clusterDim.x = 1;
-    at[n].val.clusterDim.y = 1;
-    at[n].val.clusterDim.z = cluster_z;
-    ++n;
-  }
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-#define CHAIN_LAUNCH(what, ...) \
-  do { \
-    cudaError_t e_ = launch_chain(__VA_ARGS__); \
-    if (e_ != cudaSuccess) return fail(DFSSM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e_)); \
-  } while (0)
 
 constexpr size_t kNone = ~size_t(0);
 constexpr int kHeadBlocks = 592;  // 4 per SM on a 148-SM B200
@@ -290,32 +213,6 @@ int pick_bt(int batch, int K, int rank) {
   return bt;
 }
 
-int current_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    dev = 0;
-  }
-  return dev;
-}
-
-// SM count of the current device, cached per device.
-int sm_count() {
-  static std::mutex mu;
-  static std::vector<std::array<int, 2>> cache;   // device, SMs
-  const int dev = current_device();
-  std::lock_guard<std::mutex> lock(mu);
-  for (const auto& c : cache)
-    if (c[0] == dev) return c[1];
-  int v = 0;
-  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
-    cudaGetLastError();
-    v = 148;
-  }
-  cache.push_back({dev, v});
-  return v;
-}
-
 // Resident blocks per SM of `kernel` with `threads` threads and `smem` bytes of
 // dynamic shared memory on the current device, cached per (kernel, device, smem).
 // The kernel's dynamic shared-memory limit is set to `smem` on every call (a cheap
@@ -364,21 +261,6 @@ int proj_path_override() {
   return 0;
 }
 constexpr int kTcMinBatch = 16;
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link against
-// the driver library), looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
 
 // The two TMA maps of k_proj_tc: the tiled sign words as [row tiles][K/256 x 128
 // words] (box: 8 tiles x 128 words, no swizzle) and the digit planes as
@@ -881,7 +763,7 @@ int dfssm_model_decode_launches(const dfssm_dims* d, int n_layer, int vocab) {
   return 1 + 5 * n_layer + 2;
 }
 
-const char* dfssm_last_error(void) { return g_last_error.c_str(); }
+const char* dfssm_last_error(void) { return last_error_text().c_str(); }
 
 size_t dfssm_packed_words(int rows, int cols, int layout) {
   if (rows <= 0 || cols <= 0) return 0;

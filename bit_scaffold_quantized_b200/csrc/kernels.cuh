@@ -16,6 +16,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace dfssm {
 
@@ -740,7 +741,6 @@ constexpr int kTcABufs = 4;                     // A buffers in tensor memory
 constexpr int kTcACol = 256;                    // first TMEM column of the A buffers
 constexpr int kTcTmemCols = 512;
 constexpr int kTcMaxSplit = 8;                  // CTAs of one cluster sharing K
-constexpr long long kTcSpinLimit = 1LL << 24;
 constexpr size_t kTcSmemCap = 225 * 1024;
 
 __host__ __device__ constexpr int tc_stage_bytes(int bg) {
@@ -761,42 +761,12 @@ __host__ __device__ constexpr size_t proj_tc_smem_bytes(int bg) {
   return size_t(tc_stages(bg)) * tc_stage_bytes(bg) + tc_tail_bytes(bg);
 }
 
-// Shared-memory matrix descriptor, K-major, 128-byte swizzle: start address, leading
-// byte offset 16 (unused by this layout), stride byte offset 1024, version 1.
-DFSSM_DEV uint64_t umma_desc_sw128(uint32_t saddr) {
-  return uint64_t((saddr >> 4) & 0x3fffu) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-
 // Instruction descriptor of kind::i8: D s32 (c_format 2), A and B both signed 8-bit
 // (format 1; the 0/1 sign bytes are valid s8 values, and A and B keep one type),
 // both K-major, N >> 3, M = 128 >> 4.
 template <int N>
 DFSSM_DEV constexpr uint32_t umma_idesc_s8() {
   return (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) | (uint32_t(kTcM >> 4) << 24);
-}
-
-DFSSM_DEV void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
-}
-
-DFSSM_DEV bool tc_wait(uint64_t* bar, unsigned parity, unsigned* status, int* fail) {
-  long long spins = 0;
-  while (!mbar_try_wait(bar, parity)) {
-    if (++spins > kTcSpinLimit || *reinterpret_cast<volatile int*>(fail)) {
-      if (spins > kTcSpinLimit && status) atomicOr(status, 65536u);
-      *reinterpret_cast<volatile int*>(fail) = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
-DFSSM_DEV void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               :: "r"(smem_u32(bar)) : "memory");
 }
 
 // 48 accumulator columns (one batch-row octet) of this warp's 32 TMEM lanes.

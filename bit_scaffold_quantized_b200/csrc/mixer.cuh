@@ -1,0 +1,787 @@
+// Kernels of the parts of a layer over packed prompts and single tokens: the causal
+// conv, the selective scan (all shapes) and the gated RMSNorm.  Arithmetic is fp32
+// with the running decay exponents in fp64; formulas and rules: dfssm.h.
+#pragma once
+
+#include "common.cuh"
+
+namespace dfssm {
+
+struct Rows {
+  void* p;
+  long long stride;
+};
+
+struct Seqs {
+  int n_seqs, n_rows, n_slots;
+  const int* start;
+  const int* slot;
+  const int* fresh;
+  unsigned* status;
+};
+
+constexpr unsigned kSeqBadSlot = 1u, kSeqSameSlot = 2u, kSeqBadStart = 4u;
+
+DFSSM_DEV float ldf(const float* p) { return *p; }
+DFSSM_DEV float ldf(const __half* p) { return __half2float(*p); }
+DFSSM_DEV void stf(float* p, float v) { *p = v; }
+DFSSM_DEV void stf(__half* p, float v) { *p = __float2half_rn(v); }
+
+// VEC consecutive values; VEC > 1 needs the address aligned to VEC values.
+template <int VEC>
+DFSSM_DEV void ldv(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + i);
+      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = p[i];
+  }
+}
+template <int VEC>
+DFSSM_DEV void ldv(const __half* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x; v[2 * i + 1] = f.y;
+    }
+  } else if constexpr (VEC == 4) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&q.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = __half2float(p[i]);
+  }
+}
+template <int VEC>
+DFSSM_DEV void stv(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) p[i] = v[i];
+  }
+}
+DFSSM_DEV uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int VEC>
+DFSSM_DEV void stv(__half* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_h2(v[0], v[1]), pack_h2(v[2], v[3]), pack_h2(v[4], v[5]), pack_h2(v[6], v[7]));
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_h2(v[0], v[1]), pack_h2(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) p[i] = __float2half_rn(v[i]);
+  }
+}
+
+// v / (1 + e^-v) in fp32: expf and one approximate divide (2 ulp).  A denominator past
+// 2^126 gives 0, where the exact value is below 1e-36.
+DFSSM_DEV float silu_f(float v) { return __fdividef(v, 1.f + expf(-v)); }
+
+DFSSM_DEV float softplus_f(float v) { return v > 20.f ? v : log1pf(expf(v)); }
+
+// Rows [b, e) of sequence s; false where they break the rule.
+DFSSM_DEV bool seq_rows(const Seqs& q, int s, int& b, int& e) {
+  if (!q.start) {
+    b = s;
+    e = s + 1;
+    return true;
+  }
+  b = q.start[s];
+  e = q.start[s + 1];
+  return b >= 0 && b <= e && e <= q.n_rows;
+}
+
+// The sequence whose rows hold row t if any does: the last s with start[s] <= t, or -1.
+DFSSM_DEV int seq_find(const Seqs& q, int t) {
+  int lo = 0, hi = q.n_seqs + 1;            // first index with start > t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (q.start[mid] <= t) lo = mid + 1;
+    else hi = mid;
+  }
+  return min(lo - 1, q.n_seqs - 1);
+}
+
+// Slot of sequence s, or -1 where it is left out.  `lane` of `lanes` threads share the
+// look at the earlier sequences; `any` ors their findings and returns the result to all.
+template <typename Any>
+DFSSM_DEV int seq_slot(const Seqs& q, int s, int lane, int lanes, Any any) {
+  int sl = s;
+  bool twice = false;
+  if (q.slot) {
+    sl = q.slot[s];
+    for (int j = lane; j < s; j += lanes) twice |= q.slot[j] == sl;
+    twice = any(twice && sl >= 0);
+  }
+  if (sl >= 0 && sl < q.n_slots && !twice) return sl;
+  if (lane == 0 && q.status && (twice || sl != -1)) atomicOr(q.status, twice ? kSeqSameSlot : kSeqBadSlot);
+  return -1;
+}
+
+// ------------------------------------------------------------------ causal conv
+
+struct ConvArgs {
+  Seqs q;
+  Rows x, y;
+  const uint16_t* w;
+  const uint16_t* b;
+  float* state;
+  int channels, silu, tiles, cblocks;
+};
+
+constexpr int kConvThreads = 128;
+constexpr int kConvTile = 32;       // rows of one block
+constexpr int kConvUnroll = 8;      // rows loaded ahead
+
+template <int VEC, int W>
+DFSSM_DEV void conv_weights(const ConvArgs& a, int c, float (&w)[W][VEC], float (&bias)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][i] = h2f(a.w[size_t(c + i) * W + j]);
+    bias[i] = a.b ? h2f(a.b[c + i]) : 0.f;
+  }
+}
+
+template <int VEC, int W>
+DFSSM_DEV void conv_row(const ConvArgs& a, const float (&w)[W][VEC], const float (&bias)[VEC],
+                        const float (&win)[W - 1][VEC], const float (&x)[VEC], float (&v)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    float s = bias[i];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][i], win[j][i], s);
+    s = fmaf(w[W - 1][i], x[i], s);
+    v[i] = a.silu ? silu_f(s) : s;
+  }
+}
+
+// First row that tile boundary t stands for: a boundary inside the first W - 1 rows of a
+// sequence (which need the sequence's old state) moves past them, so that one block alone
+// reads the old state and writes the new one.
+template <int W>
+DFSSM_DEV int conv_edge(const Seqs& q, int t) {
+  if (t >= q.n_rows) return q.n_rows;
+  const int s = seq_find(q, t);
+  if (s < 0) return t;
+  const int b = q.start[s], e = q.start[s + 1];
+  if (b < 0 || e > q.n_rows || t <= b || t >= e || t - b >= W - 1) return t;
+  return min(b + W - 1, e);
+}
+
+// One block: kConvTile rows of kConvThreads * VEC channels; a thread walks its channels
+// down the rows with the last W - 1 inputs in registers.
+template <typename TX, typename TY, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads) k_conv_prompt(ConvArgs a) {
+  pdl_wait();
+  pdl_release();
+  const int tile = blockIdx.x / a.cblocks, lane = threadIdx.x & 31;
+  const int c = ((blockIdx.x % a.cblocks) * kConvThreads + threadIdx.x) * VEC;
+  const bool on = c < a.channels;
+  const Seqs& q = a.q;
+  float w[W][VEC], bias[VEC];
+  if (on) conv_weights<VEC, W>(a, c, w, bias);
+  const TX* xp = static_cast<const TX*>(a.x.p) + c;
+  TY* yp = static_cast<TY*>(a.y.p) + c;
+  int r = conv_edge<W>(q, tile * kConvTile);
+  const int end = conv_edge<W>(q, min(q.n_rows, (tile + 1) * kConvTile));
+  int s = seq_find(q, r);
+  while (r < end) {
+    while (s + 1 < q.n_seqs && q.start[s + 1] <= r) ++s;
+    int b = 0, e = 0;
+    const bool fine = s >= 0 && seq_rows(q, s, b, e);
+    if (!fine || r < b || r >= e) {          // rows of no sequence
+      if (s >= 0 && !fine && lane == 0 && q.status) atomicOr(q.status, kSeqBadStart);
+      if (s + 1 >= q.n_seqs && s >= 0) break;
+      r = max(r + 1, q.start[s + 1]);
+      continue;
+    }
+    const int stop = min(e, end);
+    int slot = -1;
+    if (a.state) {
+      slot = seq_slot(q, s, lane, 32, [](bool v) { return __any_sync(0xffffffffu, v) != 0; });
+      if (slot < 0) {
+        r = stop;
+        continue;
+      }
+    }
+    if (!on) {
+      r = stop;
+      continue;
+    }
+    float win[W - 1][VEC];
+    const int pos = r - b;
+    if (pos >= W - 1) {
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) ldv<VEC>(xp + (r - (W - 1) + j) * a.x.stride, win[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
+      if (slot >= 0 && pos == 0) {
+        float* sp = a.state + size_t(slot) * (W - 1) * a.channels + c;
+        if (!(q.fresh && q.fresh[s])) {
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) ldv<VEC>(sp + size_t(j) * a.channels, win[j]);
+        }
+        // the state after the last row: the last W - 1 of the old rows and the sequence's
+        const int len = e - b;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+          float v[VEC];
+          const int k = len - (W - 1) + j;
+          if (k >= 0) {
+            ldv<VEC>(xp + (long long)(b + k) * a.x.stride, v);
+          } else {
+#pragma unroll
+            for (int m = 0; m < W - 1; ++m)
+              if (m == j + len)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[i] = win[m][i];
+          }
+          stv<VEC>(sp + size_t(j) * a.channels, v);
+        }
+      }
+    }
+    while (r < stop) {
+      float x[kConvUnroll][VEC], v[VEC];
+#pragma unroll
+      for (int u = 0; u < kConvUnroll; ++u)
+        if (r + u < stop) ldv<VEC>(xp + (long long)(r + u) * a.x.stride, x[u]);
+#pragma unroll
+      for (int u = 0; u < kConvUnroll; ++u) {
+        if (r + u < stop) {
+          conv_row<VEC, W>(a, w, bias, win, x[u], v);
+          stv<VEC>(yp + (long long)(r + u) * a.y.stride, v);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+            for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
+            win[W - 2][i] = x[u][i];
+          }
+        }
+      }
+      r += kConvUnroll;
+    }
+    r = stop;
+  }
+}
+
+// One row per sequence: grid (sequences, channel blocks).
+template <typename TX, typename TY, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads) k_conv_token(ConvArgs a) {
+  pdl_wait();
+  pdl_release();
+  const int s = blockIdx.x, c = (blockIdx.y * kConvThreads + threadIdx.x) * VEC;
+  const bool on = c < a.channels;
+  float w[W][VEC], bias[VEC], x[VEC], v[VEC], win[W - 1][VEC];
+  if (on) {
+    conv_weights<VEC, W>(a, c, w, bias);
+    ldv<VEC>(static_cast<const TX*>(a.x.p) + s * a.x.stride + c, x);
+  }
+  const int slot = seq_slot(a.q, s, threadIdx.x, kConvThreads, [](bool t) { return __syncthreads_or(t) != 0; });
+  if (slot < 0 || !on) return;
+  float* sp = a.state + size_t(slot) * (W - 1) * a.channels + c;
+  const bool fresh = a.q.fresh && a.q.fresh[s];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    if (fresh) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
+    } else {
+      ldv<VEC>(sp + size_t(j) * a.channels, win[j]);
+    }
+  }
+  conv_row<VEC, W>(a, w, bias, win, x, v);
+  stv<VEC>(static_cast<TY*>(a.y.p) + s * a.y.stride + c, v);
+#pragma unroll
+  for (int j = 0; j + 1 < W - 1; ++j) stv<VEC>(sp + size_t(j) * a.channels, win[j + 1]);
+  stv<VEC>(sp + size_t(W - 2) * a.channels, x);
+}
+
+// ------------------------------------------------------------------ selective scan
+
+struct ScanArgs {
+  Seqs q;
+  Rows x, dt, B, C, y;
+  int H, P, N, G, dt16;
+  const float* dt_bias;
+  const float* A_log;
+  const float* D;
+  void* state;
+  // prompt form: every sequence in segments of seg rows (a multiple of the chunk);
+  // with more than one segment the states between them pass through the workspace
+  int seg, max_segs;
+  float* seg_state;      // [max_segs][H][P][N]
+  float* seg_decay;      // [max_segs][H]: decay over the segment
+};
+
+DFSSM_DEV float scan_dt(const ScanArgs& a, long long row, int h) {
+  const long long at = row * a.dt.stride + h;
+  const float raw = a.dt16 ? __half2float(static_cast<const __half*>(a.dt.p)[at]) : static_cast<const float*>(a.dt.p)[at];
+  return softplus_f(raw + a.dt_bias[h]);
+}
+
+constexpr int kTokThreads = 128;
+
+// One token: block = (sequence, head, PASSES * 16 rows of the head's state).  Eight lanes
+// share a state row, four consecutive values each, NJ times; a warp has four rows.
+template <typename TX, typename TY, typename TS, int NJ, int PASSES>
+__global__ void __launch_bounds__(kTokThreads) k_scan_token(ScanArgs a) {
+  pdl_wait();
+  pdl_release();
+  const int s = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int p0 = blockIdx.z * (16 * PASSES) + warp * 4 + (lane >> 3), n0 = 4 * (lane & 7);
+  const int g = h / (a.H / a.G);
+  const int slot = seq_slot(a.q, s, tid, kTokThreads, [](bool t) { return __syncthreads_or(t) != 0; });
+  if (slot < 0) return;
+  const bool fresh = a.q.fresh && a.q.fresh[s];
+  TS* sp = static_cast<TS*>(a.state) + (size_t(slot) * a.H + h) * a.P * a.N;
+  float st[PASSES][NJ][4];
+#pragma unroll
+  for (int k = 0; k < PASSES; ++k)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int p = p0 + 16 * k, n = n0 + 32 * j;
+      if (!fresh && p < a.P && n < a.N) {
+        ldv<4>(sp + size_t(p) * a.N + n, st[k][j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st[k][j][i] = 0.f;
+      }
+    }
+  const TX* xr = static_cast<const TX*>(a.x.p) + s * a.x.stride + h * a.P;
+  const TX* br = static_cast<const TX*>(a.B.p) + s * a.B.stride + g * a.N;
+  const TX* cr = static_cast<const TX*>(a.C.p) + s * a.C.stride + g * a.N;
+  float bv[NJ][4], cv[NJ][4];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = n0 + 32 * j + i;
+      bv[j][i] = n < a.N ? ldf(br + n) : 0.f;
+      cv[j][i] = n < a.N ? ldf(cr + n) : 0.f;
+    }
+  const float dt = scan_dt(a, s, h), dA = expf(-dt * expf(a.A_log[h])), Dh = a.D ? a.D[h] : 0.f;
+#pragma unroll
+  for (int k = 0; k < PASSES; ++k) {
+    const int p = p0 + 16 * k;
+    const float x = p < a.P ? ldf(xr + p) : 0.f, u = dt * x;
+    float y = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        st[k][j][i] = fmaf(st[k][j][i], dA, u * bv[j][i]);
+        y = fmaf(st[k][j][i], cv[j][i], y);
+      }
+      const int n = n0 + 32 * j;
+      if (p < a.P && n < a.N) stv<4>(sp + size_t(p) * a.N + n, st[k][j]);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    if ((lane & 7) == 0 && p < a.P)
+      stf(static_cast<TY*>(a.y.p) + s * a.y.stride + h * a.P + p, fmaf(Dh, x, y));
+  }
+}
+
+// ---- prompts
+
+// Segment i of the call: its sequence and place.  A sequence of n rows has
+// max(1, ceil(n / seg)) segments; they are numbered through the sequences with room for
+// every possible division: segment k of sequence s is number start[s] / seg + s + k.
+// (start[s + 1] / seg + s + 1 - start[s] / seg - s >= ceil(n / seg), so numbers of
+// different sequences never meet, and the last is below n_rows / seg + n_seqs.)
+DFSSM_DEV int seg_first(const ScanArgs& a, int s, int b) { return b / a.seg + s; }
+
+struct SegWork {
+  int s, b, e;       // sequence, its rows
+  int t0, t1;        // rows of this segment
+  int k, count;      // place among the sequence's segments
+};
+
+// The segment with number i, or false if no sequence has it.
+DFSSM_DEV bool seg_find(const ScanArgs& a, int i, SegWork& w) {
+  int lo = 0, hi = a.q.n_seqs;              // first s with seg_first(s) > i
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (seg_first(a, mid, a.q.start[mid]) <= i) lo = mid + 1;
+    else hi = mid;
+  }
+  w.s = lo - 1;
+  if (w.s < 0) return false;
+  if (!seq_rows(a.q, w.s, w.b, w.e)) {
+    if (threadIdx.x == 0 && a.q.status) atomicOr(a.q.status, kSeqBadStart);
+    return false;
+  }
+  w.k = i - seg_first(a, w.s, w.b);
+  w.count = (w.e - w.b + a.seg - 1) / a.seg;
+  if (w.k < 0 || w.k >= w.count) return false;
+  w.t0 = w.b + w.k * a.seg;
+  w.t1 = min(w.e, w.t0 + a.seg);
+  return true;
+}
+
+constexpr int kScanQ = 32;           // chunk
+constexpr int kScanThreads = 256;
+
+__host__ __device__ constexpr size_t scan_smem_bytes(int P, int N) {
+  return 8 * kScanQ + 4 * (size_t(P) * (N + 4) + size_t(kScanQ) * P + 2 * size_t(kScanQ) * (N + 4) +
+                           size_t(kScanQ) * (kScanQ + 4) + 3 * kScanQ);
+}
+
+// Any shape and type.  Block = (segment, head), the segment in chunks of Q = 32 rows
+// with the head's state in shared memory: with cs_t the running sum of -dt exp(A_log),
+//   y_t = sum_{s <= t} (C_t . B_s) exp(cs_t - cs_s) dt_s x_s + exp(cs_t) C_t . state + D x_t,
+//   state <- exp(cs_Q) state + sum_s exp(cs_Q - cs_s) dt_s x_s (x) B_s.
+// STATES: only the state is wanted, from zero, of every segment but a sequence's last.
+template <typename TX, typename TY, typename TS, bool STATES>
+__global__ void __launch_bounds__(kScanThreads) k_scan_prompt(ScanArgs a) {
+  pdl_wait();
+  pdl_release();
+  extern __shared__ __align__(16) unsigned char scan_smem[];
+  const int P = a.P, N = a.N, NP = N + 4, Q = kScanQ, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  double* cs = reinterpret_cast<double*>(scan_smem);
+  float* hs = reinterpret_cast<float*>(cs + Q);        // [P][NP]
+  float* xs = hs + P * NP;                             // [Q][P]
+  float* bs = xs + Q * P;                              // [Q][NP]
+  float* ct = bs + Q * NP;                             // [Q][NP]
+  float* ms = ct + Q * NP;                             // [Q][Q + 4]
+  float* dts = ms + Q * (Q + 4);                       // [Q] step sizes
+  float* ws = dts + Q;                                 // [Q] exp(cs_Q - cs_s) dt_s
+  float* es = ws + Q;                                  // [Q] exp(cs_t)
+  const int h = blockIdx.y, g = h / (a.H / a.G);
+  SegWork w;
+  if (!seg_find(a, blockIdx.x, w)) return;
+  if (STATES && w.k == w.count - 1) return;
+  int slot = -1;
+  if (a.state) {
+    slot = seq_slot(a.q, w.s, tid, kScanThreads, [](bool v) { return __syncthreads_or(v) != 0; });
+    if (slot < 0) return;
+  }
+  TS* state = a.state ? static_cast<TS*>(a.state) + (size_t(slot) * a.H + h) * P * N : nullptr;
+  float* seg_state = a.seg_state + (size_t(blockIdx.x) * a.H + h) * P * N;
+  const bool fresh = a.q.fresh && a.q.fresh[w.s];
+  for (int i = tid; i < P * N; i += kScanThreads) {
+    float v = 0.f;
+    if (!STATES) {
+      if (w.count > 1) v = seg_state[i];
+      else if (state && !fresh) v = ldf(state + i);
+    }
+    hs[(i / N) * NP + i % N] = v;
+  }
+  const double rate = -exp(double(a.A_log[h]));
+  const float Dh = a.D ? a.D[h] : 0.f;
+  double decay = 0.0;
+  for (int t0 = w.t0; t0 < w.t1; t0 += Q) {
+    const int n = min(Q, w.t1 - t0);
+    __syncthreads();
+    for (int i = tid; i < Q * P; i += kScanThreads) {
+      const int t = i / P, p = i % P;
+      xs[i] = t < n ? ldf(static_cast<const TX*>(a.x.p) + (t0 + t) * a.x.stride + h * P + p) : 0.f;
+    }
+    for (int i = tid; i < Q * N; i += kScanThreads) {
+      const int t = i / N, j = i % N;
+      bs[t * NP + j] = t < n ? ldf(static_cast<const TX*>(a.B.p) + (t0 + t) * a.B.stride + g * N + j) : 0.f;
+      if (!STATES) ct[t * NP + j] = t < n ? ldf(static_cast<const TX*>(a.C.p) + (t0 + t) * a.C.stride + g * N + j) : 0.f;
+    }
+    if (warp == 0) {
+      const float dt = lane < n ? scan_dt(a, t0 + lane, h) : 0.f;
+      double c = double(dt) * rate;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += v;
+      }
+      const double all = __shfl_sync(0xffffffffu, c, 31);
+      cs[lane] = c;
+      dts[lane] = dt;
+      ws[lane] = expf(float(all - c)) * dt;
+      es[lane] = expf(float(c));
+    }
+    __syncthreads();
+    const double total = cs[Q - 1];
+    decay += total;
+    if (!STATES) {
+      // M[t][s] = (C_t . B_s) exp(cs_t - cs_s) dt_s for s <= t: thread = (t, four s)
+      const int t = tid >> 3;
+      float m[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < N; j += 4) {
+        const float4 cv = *reinterpret_cast<const float4*>(ct + t * NP + j);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 bv = *reinterpret_cast<const float4*>(bs + ((tid & 7) + 8 * k) * NP + j);
+          m[k] = fmaf(cv.x, bv.x, fmaf(cv.y, bv.y, fmaf(cv.z, bv.z, fmaf(cv.w, bv.w, m[k]))));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int s = (tid & 7) + 8 * k;
+        ms[t * (Q + 4) + s] = s <= t ? m[k] * expf(float(cs[t] - cs[s])) * dts[s] : 0.f;
+      }
+      __syncthreads();
+      // y: warp = four rows, lane = columns lane, lane + 32, ...
+      for (int p = lane; p < P; p += 32) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < N; j += 4) {
+          const float4 hv = *reinterpret_cast<const float4*>(hs + p * NP + j);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 cv = *reinterpret_cast<const float4*>(ct + (4 * warp + k) * NP + j);
+            acc[k] = fmaf(cv.x, hv.x, fmaf(cv.y, hv.y, fmaf(cv.z, hv.z, fmaf(cv.w, hv.w, acc[k]))));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] *= es[4 * warp + k];
+        for (int s = 0; s < 4 * warp + 4; ++s) {
+          const float xv = xs[s * P + p];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[k] = fmaf(ms[(4 * warp + k) * (Q + 4) + s], xv, acc[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int t = 4 * warp + k;
+          if (t < n)
+            stf(static_cast<TY*>(a.y.p) + (t0 + t) * a.y.stride + h * P + p, fmaf(Dh, xs[t * P + p], acc[k]));
+        }
+      }
+      __syncthreads();
+    }
+    // state: item = 8 rows x 4 columns
+    const float keep = expf(float(total));
+    for (int it = tid; it < (P / 8) * (N / 4); it += kScanThreads) {
+      const int p = 8 * (it / (N / 4)), j = 4 * (it % (N / 4));
+      float4 acc[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(hs + (p + k) * NP + j);
+        acc[k] = make_float4(v.x * keep, v.y * keep, v.z * keep, v.w * keep);
+      }
+      for (int s = 0; s < n; ++s) {
+        float4 bv = *reinterpret_cast<const float4*>(bs + s * NP + j);
+        const float wv = ws[s];
+        bv.x *= wv; bv.y *= wv; bv.z *= wv; bv.w *= wv;
+        const float4 xa = *reinterpret_cast<const float4*>(xs + s * P + p);
+        const float4 xb = *reinterpret_cast<const float4*>(xs + s * P + p + 4);
+        const float xv[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          acc[k].x = fmaf(xv[k], bv.x, acc[k].x);
+          acc[k].y = fmaf(xv[k], bv.y, acc[k].y);
+          acc[k].z = fmaf(xv[k], bv.z, acc[k].z);
+          acc[k].w = fmaf(xv[k], bv.w, acc[k].w);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) *reinterpret_cast<float4*>(hs + (p + k) * NP + j) = acc[k];
+    }
+  }
+  __syncthreads();
+  if (STATES) {
+    for (int i = tid; i < P * N; i += kScanThreads) seg_state[i] = hs[(i / N) * NP + i % N];
+    if (tid == 0) a.seg_decay[size_t(blockIdx.x) * a.H + h] = expf(float(decay));
+  } else if (state && w.k == w.count - 1) {
+    for (int i = tid; i < P * N; i += kScanThreads) stf(state + i, hs[(i / N) * NP + i % N]);
+  }
+}
+
+// The states between segments: thread = four values of one head's state of one sequence;
+// segment k's own state (from zero) gives way to the state that enters segment k.
+template <typename TS>
+__global__ void __launch_bounds__(256) k_scan_join(ScanArgs a) {
+  pdl_wait();
+  pdl_release();
+  const int s = blockIdx.x, h = blockIdx.y, i = 4 * (blockIdx.z * 256 + threadIdx.x);
+  int b, e;
+  if (!seq_rows(a.q, s, b, e)) return;
+  const int count = (e - b + a.seg - 1) / a.seg;
+  if (count <= 1) return;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (a.state) {
+    const int slot = seq_slot(a.q, s, threadIdx.x, 256, [](bool t) { return __syncthreads_or(t) != 0; });
+    if (slot < 0) return;
+    if (i < a.P * a.N && !(a.q.fresh && a.q.fresh[s]))
+      ldv<4>(static_cast<const TS*>(a.state) + (size_t(slot) * a.H + h) * a.P * a.N + i, v);
+  }
+  if (i >= a.P * a.N) return;
+  const int first = seg_first(a, s, b);
+  for (int k = 0; k < count; ++k) {
+    float* at = a.seg_state + (size_t(first + k) * a.H + h) * a.P * a.N + i;
+    float own[4] = {0.f, 0.f, 0.f, 0.f}, d = 0.f;
+    if (k + 1 < count) {
+      ldv<4>(at, own);
+      d = a.seg_decay[size_t(first + k) * a.H + h];
+    }
+    stv<4>(at, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], d, own[j]);
+  }
+}
+
+// ------------------------------------------------------------------ gated RMSNorm
+
+struct NormArgs {
+  int cols, groups;
+  long long parts;       // rows * groups
+  Rows y, z, out;
+  const uint16_t* w;
+};
+
+constexpr int kNormThreads = 256;
+
+// THREADS threads (a warp or the block) per part of gs = cols / groups values, held in
+// registers: NV pieces of VEC per thread.
+template <typename TY, typename TZ, typename TO, int VEC, int THREADS, int NV>
+__global__ void __launch_bounds__(kNormThreads) k_gated_norm(NormArgs a) {
+  pdl_wait();
+  pdl_release();
+  __shared__ float red[kNormThreads / 32];
+  const int t = threadIdx.x % THREADS, gs = a.cols / a.groups;
+  const long long part = (long long)blockIdx.x * (kNormThreads / THREADS) + threadIdx.x / THREADS;
+  if (part >= a.parts) return;      // whole warps: THREADS is 32 or the block
+  const long long row = part / a.groups;
+  const int c0 = int(part % a.groups) * gs;
+  const TY* yp = static_cast<const TY*>(a.y.p) + row * a.y.stride + c0;
+  const TZ* zp = a.z.p ? static_cast<const TZ*>(a.z.p) + row * a.z.stride + c0 : nullptr;
+  TO* op = static_cast<TO*>(a.out.p) + row * a.out.stride + c0;
+  float v[NV][VEC], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (t + THREADS * k) * VEC;
+    if (c < gs) {
+      ldv<VEC>(yp + c, v[k]);
+      if (zp) {
+        float z[VEC];
+        ldv<VEC>(zp + c, z);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[k][i] *= silu_f(z[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) sum = fmaf(v[k][i], v[k][i], sum);
+    }
+  }
+  sum = warp_sum(sum);
+  if (THREADS > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNormThreads / 32; ++i) sum += red[i];
+  }
+  const float rs = rsqrtf(sum / float(gs) + kEps);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (t + THREADS * k) * VEC;
+    if (c < gs) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[k][i] = v[k][i] * rs * h2f(a.w[c0 + c + i]);
+      stv<VEC>(op + c, v[k]);
+    }
+  }
+}
+
+// Parts of any length: one block per part, y and z read twice.
+template <typename TY, typename TZ, typename TO>
+__global__ void __launch_bounds__(kNormThreads) k_gated_norm_long(NormArgs a) {
+  pdl_wait();
+  pdl_release();
+  __shared__ float red[kNormThreads / 32];
+  const int gs = a.cols / a.groups;
+  const long long part = blockIdx.x, row = part / a.groups;
+  const int c0 = int(part % a.groups) * gs;
+  const TY* yp = static_cast<const TY*>(a.y.p) + row * a.y.stride + c0;
+  const TZ* zp = a.z.p ? static_cast<const TZ*>(a.z.p) + row * a.z.stride + c0 : nullptr;
+  TO* op = static_cast<TO*>(a.out.p) + row * a.out.stride + c0;
+  float sum = 0.f;
+  for (int c = threadIdx.x; c < gs; c += kNormThreads) {
+    const float v = ldf(yp + c) * (zp ? silu_f(ldf(zp + c)) : 1.f);
+    sum = fmaf(v, v, sum);
+  }
+  sum = warp_sum(sum);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kNormThreads / 32; ++i) sum += red[i];
+  const float rs = rsqrtf(sum / float(gs) + kEps);
+  for (int c = threadIdx.x; c < gs; c += kNormThreads) {
+    const float v = ldf(yp + c) * (zp ? silu_f(ldf(zp + c)) : 1.f);
+    stf(op + c, v * rs * h2f(a.w[c0 + c]));
+  }
+}
+
+// ------------------------------------------------------------------ dense projection
+
+struct DenseArgs {
+  int rows, cols, batch, silu, y16, r16;
+  const uint16_t* w;
+  const uint16_t* b;
+  Rows x, r, y;
+};
+
+// The epilogue of one output: bias, activation, residual, store.
+DFSSM_DEV void dense_store(const DenseArgs& a, int i, int o, float v, float bias) {
+  v += bias;
+  if (a.silu) v = silu_f(v);
+  if (a.r.p) {
+    const long long at = i * a.r.stride + o;
+    v += a.r16 ? __half2float(static_cast<const __half*>(a.r.p)[at]) : static_cast<const float*>(a.r.p)[at];
+  }
+  const long long at = i * a.y.stride + o;
+  if (a.y16) static_cast<__half*>(a.y.p)[at] = __float2half_rn(v);
+  else static_cast<float*>(a.y.p)[at] = v;
+}
+
+constexpr int kDenseTile = 64, kDenseK = 16;
+
+// Any alignment: 64 x 64 outputs per block, 4 x 4 per thread, fp32 FMA.
+__global__ void __launch_bounds__(256) k_dense_any(DenseArgs a) {
+  pdl_wait();
+  pdl_release();
+  __shared__ float xs[kDenseK][kDenseTile + 4], ws[kDenseK][kDenseTile + 4];
+  const int tid = threadIdx.x, o0 = blockIdx.x * kDenseTile, i0 = blockIdx.y * kDenseTile;
+  const int to = 4 * (tid & 15), ti = 4 * (tid >> 4);
+  const __half* xp = static_cast<const __half*>(a.x.p);
+  const __half* wp = reinterpret_cast<const __half*>(a.w);
+  float acc[4][4] = {};
+  for (int k0 = 0; k0 < a.cols; k0 += kDenseK) {
+    __syncthreads();
+    for (int i = tid; i < kDenseTile * kDenseK; i += 256) {
+      const int r = i / kDenseK, k = i % kDenseK;
+      const bool kv = k0 + k < a.cols;
+      xs[k][r] = kv && i0 + r < a.batch ? __half2float(xp[(long long)(i0 + r) * a.x.stride + k0 + k]) : 0.f;
+      ws[k][r] = kv && o0 + r < a.rows ? __half2float(wp[(long long)(o0 + r) * a.cols + k0 + k]) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kDenseK; ++k)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) acc[m][n] = fmaf(xs[k][ti + m], ws[k][to + n], acc[m][n]);
+  }
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (i0 + ti + m < a.batch && o0 + to + n < a.rows)
+        dense_store(a, i0 + ti + m, o0 + to + n, acc[m][n], a.b ? h2f(a.b[o0 + to + n]) : 0.f);
+}
+
+}  // namespace dfssm

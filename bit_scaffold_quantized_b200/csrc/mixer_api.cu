@@ -1,0 +1,372 @@
+// C ABI of the parts of a layer (packed prompts, single tokens, dense projections):
+// host-side checks and launches.  Declarations and semantics: dfssm.h.
+#include <algorithm>
+#include <climits>
+#include <cstring>
+
+#include "dfssm.h"
+#include "host.cuh"
+#include "mixer.cuh"
+
+using namespace dfssm;
+
+namespace {
+
+size_t type_size(int dtype) { return dtype == DFSSM_DTYPE_F16 ? 2 : 4; }
+
+int check_rows(const dfssm_rows* r, const char* name, long long width, bool half_only = false) {
+  REQUIRE(r != nullptr && r->data != nullptr, DFSSM_ERR_INVALID_ARG, "%s is NULL", name);
+  REQUIRE(r->dtype == DFSSM_DTYPE_F16 || r->dtype == DFSSM_DTYPE_F32, DFSSM_ERR_INVALID_ARG, "%s: bad dtype %d", name,
+          r->dtype);
+  REQUIRE(!half_only || r->dtype == DFSSM_DTYPE_F16, DFSSM_ERR_INVALID_ARG, "%s must be fp16", name);
+  REQUIRE(r->stride >= width && r->stride <= (int64_t(1) << 40), DFSSM_ERR_INVALID_ARG,
+          "%s: stride %lld is not in [%lld, 2^40]", name, (long long)r->stride, width);
+  REQUIRE(reinterpret_cast<uintptr_t>(r->data) % type_size(r->dtype) == 0, DFSSM_ERR_MISALIGNED,
+          "%s is not aligned to its type", name);
+  return DFSSM_OK;
+}
+
+// Whether every row of r can be read and written in pieces of `values` values.
+bool rows_in_pieces(const dfssm_rows* r, int values) {
+  const size_t piece = std::min<size_t>(16, values * type_size(r->dtype));
+  return reinterpret_cast<uintptr_t>(r->data) % piece == 0 && size_t(r->stride) * type_size(r->dtype) % piece == 0;
+}
+
+int check_seqs(const dfssm_seqs* q, bool token, bool state) {
+  REQUIRE(q != nullptr, DFSSM_ERR_INVALID_ARG, "seqs is NULL");
+  REQUIRE(q->n_seqs >= 0 && q->n_rows >= 0, DFSSM_ERR_INVALID_ARG, "n_seqs (%d) and n_rows (%d) must not be negative",
+          q->n_seqs, q->n_rows);
+  REQUIRE(q->n_seqs <= 1 << 24 && q->n_rows <= 1 << 30, DFSSM_ERR_UNSUPPORTED_SHAPE,
+          "n_seqs (%d) > 2^24 or n_rows (%d) > 2^30", q->n_seqs, q->n_rows);
+  const void* ptrs[] = {q->start, q->slot, q->fresh, q->status};
+  for (const void* p : ptrs)
+    REQUIRE(reinterpret_cast<uintptr_t>(p) % 4 == 0, DFSSM_ERR_MISALIGNED,
+            "start, slot, fresh and status must be 4-byte aligned");
+  if (token) {
+    REQUIRE(q->start == nullptr, DFSSM_ERR_INVALID_ARG, "start must be NULL for single tokens");
+    REQUIRE(q->n_rows == q->n_seqs, DFSSM_ERR_INVALID_ARG, "single tokens: n_rows (%d) != n_seqs (%d)", q->n_rows,
+            q->n_seqs);
+  } else {
+    REQUIRE(q->start != nullptr, DFSSM_ERR_INVALID_ARG, "start is NULL");
+  }
+  if (state) {
+    REQUIRE(q->n_slots >= 0, DFSSM_ERR_INVALID_ARG, "n_slots (%d) must not be negative", q->n_slots);
+    REQUIRE(q->slot != nullptr || q->n_slots >= q->n_seqs, DFSSM_ERR_INVALID_ARG,
+            "n_slots (%d) < n_seqs (%d) without slot numbers", q->n_slots, q->n_seqs);
+  }
+  return DFSSM_OK;
+}
+
+Rows dev_rows(const dfssm_rows* r) { return r ? Rows{r->data, (long long)r->stride} : Rows{nullptr, 0}; }
+
+Seqs dev_seqs(const dfssm_seqs* q) {
+  return Seqs{q->n_seqs, q->n_rows, q->n_slots, q->start, q->slot, q->fresh, q->status};
+}
+
+// f(x type, y type) with the element types of two row matrices.
+template <typename F>
+int by_types(int x, int y, F f) {
+  if (x == DFSSM_DTYPE_F16) return y == DFSSM_DTYPE_F16 ? f(__half{}, __half{}) : f(__half{}, float{});
+  return y == DFSSM_DTYPE_F16 ? f(float{}, __half{}) : f(float{}, float{});
+}
+
+// ---- conv
+
+template <typename TX, typename TY, int VEC, int W>
+int conv_launch(ConvArgs a, bool token, cudaStream_t st) {
+  const int cblocks = (a.channels + kConvThreads * VEC - 1) / (kConvThreads * VEC);
+  if (token) {
+    REQUIRE(cblocks <= 65535, DFSSM_ERR_UNSUPPORTED_SHAPE, "channels (%d) out of range", a.channels);
+    CHAIN_LAUNCH("k_conv_token", k_conv_token<TX, TY, VEC, W>, dim3(a.q.n_seqs, cblocks), dim3(kConvThreads), 0, st, 0, a);
+    return DFSSM_OK;
+  }
+  a.cblocks = cblocks;
+  const long long blocks = (long long)cblocks * ((a.q.n_rows + kConvTile - 1) / kConvTile);
+  REQUIRE(blocks <= INT_MAX, DFSSM_ERR_UNSUPPORTED_SHAPE, "n_rows (%d) x channels (%d) out of range", a.q.n_rows, a.channels);
+  CHAIN_LAUNCH("k_conv_prompt", k_conv_prompt<TX, TY, VEC, W>, dim3(unsigned(blocks)), dim3(kConvThreads), 0, st, 0, a);
+  return DFSSM_OK;
+}
+
+int conv(int channels, int d_conv, int silu, const dfssm_rows* x, const uint16_t* w, const uint16_t* b,
+         const dfssm_seqs* seqs, float* state, const dfssm_rows* y, bool token, void* stream) {
+  REQUIRE(channels > 0, DFSSM_ERR_INVALID_ARG, "channels (%d) must be positive", channels);
+  REQUIRE(d_conv >= 2 && d_conv <= 4, DFSSM_ERR_UNSUPPORTED_SHAPE, "d_conv (%d) must be 2, 3 or 4", d_conv);
+  int rc;
+  if ((rc = check_rows(x, "x", channels)) || (rc = check_rows(y, "y", channels))) return rc;
+  REQUIRE_PTR(w);
+  REQUIRE(b == nullptr || aligned16(b), DFSSM_ERR_MISALIGNED, "b is not 16-byte aligned");
+  if (token) REQUIRE(state != nullptr, DFSSM_ERR_INVALID_ARG, "conv_state is NULL");
+  REQUIRE(aligned16(state), DFSSM_ERR_MISALIGNED, "conv_state is not 16-byte aligned");
+  if ((rc = check_seqs(seqs, token, state != nullptr))) return rc;
+  if (seqs->n_seqs == 0 || seqs->n_rows == 0) return ok();
+  ConvArgs a{};
+  a.q = dev_seqs(seqs);
+  a.x = dev_rows(x); a.y = dev_rows(y);
+  a.w = w; a.b = b; a.state = state; a.channels = channels; a.silu = silu != 0;
+  const bool vec = channels % 4 == 0 && rows_in_pieces(x, 4) && rows_in_pieces(y, 4);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = by_types(x->dtype, y->dtype, [&](auto tx, auto ty) {
+    using TX = decltype(tx);
+    using TY = decltype(ty);
+    switch (d_conv) {
+      case 2: return vec ? conv_launch<TX, TY, 4, 2>(a, token, st) : conv_launch<TX, TY, 1, 2>(a, token, st);
+      case 3: return vec ? conv_launch<TX, TY, 4, 3>(a, token, st) : conv_launch<TX, TY, 1, 3>(a, token, st);
+      default: return vec ? conv_launch<TX, TY, 4, 4>(a, token, st) : conv_launch<TX, TY, 1, 4>(a, token, st);
+    }
+  });
+  return rc ? rc : ok();
+}
+
+// ---- scan
+
+int check_scan(const dfssm_scan* s) {
+  REQUIRE(s != nullptr, DFSSM_ERR_INVALID_ARG, "scan is NULL");
+  REQUIRE(s->nheads > 0 && s->headdim > 0 && s->d_state > 0 && s->ngroups > 0, DFSSM_ERR_INVALID_ARG,
+          "nheads, headdim, d_state and ngroups must be positive");
+  REQUIRE(s->nheads % s->ngroups == 0, DFSSM_ERR_UNSUPPORTED_SHAPE, "nheads (%d) is not a multiple of ngroups (%d)",
+          s->nheads, s->ngroups);
+  REQUIRE(s->nheads <= 65535, DFSSM_ERR_UNSUPPORTED_SHAPE, "nheads (%d) > 65535", s->nheads);
+  REQUIRE(s->headdim % 16 == 0 && s->headdim <= 128, DFSSM_ERR_UNSUPPORTED_SHAPE,
+          "headdim (%d) must be a multiple of 16 and <= 128", s->headdim);
+  REQUIRE(s->d_state % 4 == 0 && s->d_state <= 256, DFSSM_ERR_UNSUPPORTED_SHAPE,
+          "d_state (%d) must be a multiple of 4 and <= 256", s->d_state);
+  REQUIRE(s->state_dtype == DFSSM_DTYPE_F16 || s->state_dtype == DFSSM_DTYPE_F32, DFSSM_ERR_INVALID_ARG,
+          "bad state_dtype %d", s->state_dtype);
+  return DFSSM_OK;
+}
+
+// Segments of the prompt form: enough (segment, head) blocks for about four per SM, and
+// no shorter than four chunks, below which the states between segments cost more to
+// move than the rows.
+struct ScanPlan {
+  int seg, max_segs;
+  size_t decay_at, bytes;
+};
+
+ScanPlan scan_plan(const dfssm_scan* s, int n_seqs, int n_rows) {
+  ScanPlan p;
+  const long long want = 4LL * sm_count();
+  long long seg = ((long long)n_rows * s->nheads + want - 1) / want;
+  seg = std::max<long long>(4 * kScanQ, (seg + kScanQ - 1) / kScanQ * kScanQ);
+  if (seg >= n_rows) {
+    p.seg = int(seg);
+    p.max_segs = n_seqs;
+    p.decay_at = p.bytes = 0;
+    return p;
+  }
+  p.seg = int(seg);
+  p.max_segs = n_rows / p.seg + n_seqs;
+  p.decay_at = (size_t(4) * p.max_segs * s->nheads * s->headdim * s->d_state + 255) & ~size_t(255);
+  p.bytes = p.decay_at + size_t(4) * p.max_segs * s->nheads;
+  return p;
+}
+
+int check_scan_call(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* dt, const dfssm_rows* B,
+                    const dfssm_rows* C, const dfssm_seqs* seqs, void* state, const dfssm_rows* y, bool token) {
+  int rc;
+  if ((rc = check_scan(s))) return rc;
+  const long long E = (long long)s->nheads * s->headdim, GN = (long long)s->ngroups * s->d_state;
+  if ((rc = check_rows(x, "x", E)) || (rc = check_rows(dt, "dt", s->nheads)) || (rc = check_rows(B, "B", GN)) ||
+      (rc = check_rows(C, "C", GN)) || (rc = check_rows(y, "y", E)))
+    return rc;
+  REQUIRE(x->dtype == B->dtype && x->dtype == C->dtype, DFSSM_ERR_INVALID_ARG, "x, B and C must have one dtype");
+  REQUIRE_PTR(s->dt_bias);
+  REQUIRE_PTR(s->A_log);
+  REQUIRE(aligned16(s->D), DFSSM_ERR_MISALIGNED, "D is not 16-byte aligned");
+  if (token) REQUIRE(state != nullptr, DFSSM_ERR_INVALID_ARG, "state is NULL");
+  REQUIRE(aligned16(state), DFSSM_ERR_MISALIGNED, "state is not 16-byte aligned");
+  return check_seqs(seqs, token, state != nullptr);
+}
+
+ScanArgs scan_args(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* dt, const dfssm_rows* B,
+                   const dfssm_rows* C, const dfssm_seqs* seqs, void* state, const dfssm_rows* y) {
+  ScanArgs a{};
+  a.q = dev_seqs(seqs);
+  a.x = dev_rows(x); a.dt = dev_rows(dt); a.B = dev_rows(B); a.C = dev_rows(C); a.y = dev_rows(y);
+  a.H = s->nheads; a.P = s->headdim; a.N = s->d_state; a.G = s->ngroups; a.dt16 = dt->dtype == DFSSM_DTYPE_F16;
+  a.dt_bias = s->dt_bias; a.A_log = s->A_log; a.D = s->D; a.state = state;
+  return a;
+}
+
+template <typename TX, typename TY, typename TS>
+int scan_token_launch(const ScanArgs& a, cudaStream_t st) {
+  // one pass of 16 state rows per block while there are few blocks, four from there on
+  const bool few = (long long)a.q.n_seqs * a.H * a.P <= 16LL * 4 * 4 * sm_count();
+  const int rows = few ? 16 : 64;
+  const dim3 grid(a.q.n_seqs, a.H, (a.P + rows - 1) / rows);
+  auto go = [&](auto nj) {
+    constexpr int NJ = decltype(nj)::value;
+    if (few) CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, NJ, 1>, grid, dim3(kTokThreads), 0, st, 0, a);
+    else CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, NJ, 4>, grid, dim3(kTokThreads), 0, st, 0, a);
+    return int(DFSSM_OK);
+  };
+  if (a.N <= 32) return go(std::integral_constant<int, 1>{});
+  if (a.N <= 64) return go(std::integral_constant<int, 2>{});
+  if (a.N <= 128) return go(std::integral_constant<int, 4>{});
+  return go(std::integral_constant<int, 8>{});
+}
+
+template <typename TX, typename TY, typename TS>
+int scan_prompt_launch(const ScanArgs& a, cudaStream_t st) {
+  const size_t smem = scan_smem_bytes(a.P, a.N);
+  auto attr = [&](auto kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  };
+  cudaError_t e = attr(k_scan_prompt<TX, TY, TS, false>);
+  if (e == cudaSuccess) e = attr(k_scan_prompt<TX, TY, TS, true>);
+  if (e != cudaSuccess) return fail(DFSSM_ERR_CUDA, "k_scan_prompt smem attribute: %s", cudaGetErrorString(e));
+  const dim3 grid(a.max_segs, a.H);
+  if (a.seg_state) {
+    CHAIN_LAUNCH("k_scan_prompt", k_scan_prompt<TX, TY, TS, true>, grid, dim3(kScanThreads), smem, st, 0, a);
+    CHAIN_LAUNCH("k_scan_join", k_scan_join<TS>, dim3(a.q.n_seqs, a.H, (a.P * a.N + 1023) / 1024), dim3(256), 0, st, 0, a);
+  }
+  CHAIN_LAUNCH("k_scan_prompt", k_scan_prompt<TX, TY, TS, false>, grid, dim3(kScanThreads), smem, st, 0, a);
+  return DFSSM_OK;
+}
+
+// ---- norm
+
+template <typename TY, typename TZ, typename TO>
+int norm_launch(const NormArgs& a, bool vec, cudaStream_t st) {
+  const int gs = a.cols / a.groups;
+  auto go = [&](auto kernel, int threads) {
+    const long long blocks = (a.parts + kNormThreads / threads - 1) / (kNormThreads / threads);
+    CHAIN_LAUNCH("k_gated_norm", kernel, dim3(unsigned(blocks)), dim3(kNormThreads), 0, st, 0, a);
+    return int(DFSSM_OK);
+  };
+  if (vec) {
+    if (gs <= 256) return go(k_gated_norm<TY, TZ, TO, 8, 32, 1>, 32);
+    if (gs <= 1024) return go(k_gated_norm<TY, TZ, TO, 8, 32, 4>, 32);
+    if (gs <= 2048) return go(k_gated_norm<TY, TZ, TO, 8, 256, 1>, 256);
+    if (gs <= 4096) return go(k_gated_norm<TY, TZ, TO, 8, 256, 2>, 256);
+    if (gs <= 8192) return go(k_gated_norm<TY, TZ, TO, 8, 256, 4>, 256);
+  } else if (gs <= 512) {
+    return go(k_gated_norm<TY, TZ, TO, 1, 32, 16>, 32);
+  }
+  return go(k_gated_norm_long<TY, TZ, TO>, kNormThreads);
+}
+
+}  // namespace
+
+extern "C" {
+
+int dfssm_conv_prompt(int channels, int d_conv, int silu, const dfssm_rows* x, const uint16_t* w, const uint16_t* b,
+                      const dfssm_seqs* seqs, float* conv_state, const dfssm_rows* y, void* stream) {
+  return conv(channels, d_conv, silu, x, w, b, seqs, conv_state, y, false, stream);
+}
+
+int dfssm_conv_token(int channels, int d_conv, int silu, const dfssm_rows* x, const uint16_t* w, const uint16_t* b,
+                     const dfssm_seqs* seqs, float* conv_state, const dfssm_rows* y, void* stream) {
+  return conv(channels, d_conv, silu, x, w, b, seqs, conv_state, y, true, stream);
+}
+
+size_t dfssm_scan_workspace_bytes(const dfssm_scan* s, int dtype, int n_seqs, int n_rows) {
+  if (check_scan(s)) return 0;
+  if ((dtype != DFSSM_DTYPE_F16 && dtype != DFSSM_DTYPE_F32) || n_seqs < 0 || n_rows < 0) {
+    fail(DFSSM_ERR_INVALID_ARG, "scan workspace: bad dtype (%d), n_seqs (%d) or n_rows (%d)", dtype, n_seqs, n_rows);
+    return 0;
+  }
+  ok();
+  return std::max<size_t>(16, scan_plan(s, n_seqs, n_rows).bytes);
+}
+
+int dfssm_scan_prompt(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* dt, const dfssm_rows* B,
+                      const dfssm_rows* C, const dfssm_seqs* seqs, void* state, const dfssm_rows* y, void* ws,
+                      size_t ws_bytes, void* stream) {
+  int rc = check_scan_call(s, x, dt, B, C, seqs, state, y, false);
+  if (rc) return rc;
+  REQUIRE_PTR(ws);
+  const size_t need = dfssm_scan_workspace_bytes(s, x->dtype, seqs->n_seqs, seqs->n_rows);
+  REQUIRE(ws_bytes >= need, DFSSM_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", ws_bytes, need);
+  if (seqs->n_seqs == 0 || seqs->n_rows == 0) return ok();
+  ScanArgs a = scan_args(s, x, dt, B, C, seqs, state, y);
+  const ScanPlan p = scan_plan(s, seqs->n_seqs, seqs->n_rows);
+  a.seg = p.seg;
+  a.max_segs = p.max_segs;
+  if (p.bytes) {
+    a.seg_state = static_cast<float*>(ws);
+    a.seg_decay = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + p.decay_at);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = by_types(x->dtype, y->dtype, [&](auto tx, auto ty) {
+    using TX = decltype(tx);
+    using TY = decltype(ty);
+    return s->state_dtype == DFSSM_DTYPE_F16 ? scan_prompt_launch<TX, TY, __half>(a, st)
+                                             : scan_prompt_launch<TX, TY, float>(a, st);
+  });
+  return rc ? rc : ok();
+}
+
+int dfssm_scan_token(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* dt, const dfssm_rows* B,
+                     const dfssm_rows* C, const dfssm_seqs* seqs, void* state, const dfssm_rows* y, void* stream) {
+  int rc = check_scan_call(s, x, dt, B, C, seqs, state, y, true);
+  if (rc) return rc;
+  if (seqs->n_seqs == 0) return ok();
+  const ScanArgs a = scan_args(s, x, dt, B, C, seqs, state, y);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = by_types(x->dtype, y->dtype, [&](auto tx, auto ty) {
+    using TX = decltype(tx);
+    using TY = decltype(ty);
+    return s->state_dtype == DFSSM_DTYPE_F16 ? scan_token_launch<TX, TY, __half>(a, st)
+                                             : scan_token_launch<TX, TY, float>(a, st);
+  });
+  return rc ? rc : ok();
+}
+
+int dfssm_gated_norm(int rows, int cols, int ngroups, const dfssm_rows* y, const dfssm_rows* z, const uint16_t* w,
+                     const dfssm_rows* out, void* stream) {
+  REQUIRE(rows >= 0 && cols > 0 && ngroups > 0, DFSSM_ERR_INVALID_ARG, "rows (%d), cols (%d) or ngroups (%d) out of range",
+          rows, cols, ngroups);
+  REQUIRE(cols % ngroups == 0, DFSSM_ERR_UNSUPPORTED_SHAPE, "cols (%d) is not a multiple of ngroups (%d)", cols, ngroups);
+  int rc;
+  if ((rc = check_rows(y, "y", cols)) || (rc = check_rows(out, "out", cols))) return rc;
+  if (z && (rc = check_rows(z, "z", cols))) return rc;
+  REQUIRE_PTR(w);
+  const dfssm_rows* in[] = {y, z};
+  for (const dfssm_rows* r : in)
+    REQUIRE(!r || r->data != out->data || (r->dtype == out->dtype && r->stride == out->stride), DFSSM_ERR_INVALID_ARG,
+            "out shares its data with an input of another dtype or stride");
+  REQUIRE((long long)rows * ngroups <= INT_MAX, DFSSM_ERR_UNSUPPORTED_SHAPE, "rows (%d) x ngroups (%d) out of range", rows,
+          ngroups);
+  if (rows == 0) return ok();
+  NormArgs a{};
+  a.cols = cols; a.groups = ngroups; a.parts = (long long)rows * ngroups;
+  a.y = dev_rows(y); a.z = dev_rows(z); a.out = dev_rows(out); a.w = w;
+  const bool vec = cols / ngroups % 8 == 0 && rows_in_pieces(y, 8) && rows_in_pieces(out, 8) && (!z || rows_in_pieces(z, 8));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = by_types(y->dtype, out->dtype, [&](auto ty, auto to) {
+    using TY = decltype(ty);
+    using TO = decltype(to);
+    return (z ? z->dtype : y->dtype) == DFSSM_DTYPE_F16 ? norm_launch<TY, __half, TO>(a, vec, st)
+                                                        : norm_launch<TY, float, TO>(a, vec, st);
+  });
+  return rc ? rc : ok();
+}
+
+int dfssm_dense_forward(int rows, int cols, int batch, const uint16_t* w, const uint16_t* b, int silu,
+                        const dfssm_rows* x, const dfssm_rows* residual, const dfssm_rows* y, void* stream) {
+  REQUIRE(rows > 0 && cols > 0 && batch >= 0, DFSSM_ERR_INVALID_ARG, "rows (%d), cols (%d) or batch (%d) out of range", rows,
+          cols, batch);
+  REQUIRE_PTR(w);
+  REQUIRE(aligned16(b), DFSSM_ERR_MISALIGNED, "b is not 16-byte aligned");
+  int rc;
+  if ((rc = check_rows(x, "x", cols, true)) || (rc = check_rows(y, "y", rows))) return rc;
+  if (residual) {
+    if ((rc = check_rows(residual, "residual", rows))) return rc;
+    REQUIRE(residual->data != y->data || (residual->dtype == y->dtype && residual->stride == y->stride),
+            DFSSM_ERR_INVALID_ARG, "y shares its data with a residual of another dtype or stride");
+  }
+  if (batch == 0) return ok();
+  DenseArgs a{};
+  a.rows = rows; a.cols = cols; a.batch = batch; a.silu = silu != 0;
+  a.w = w; a.b = b; a.x = dev_rows(x); a.r = dev_rows(residual); a.y = dev_rows(y);
+  a.y16 = y->dtype == DFSSM_DTYPE_F16;
+  a.r16 = residual && residual->dtype == DFSSM_DTYPE_F16;
+  const long long ti = (batch + kDenseTile - 1) / kDenseTile;
+  REQUIRE(ti <= 65535, DFSSM_ERR_UNSUPPORTED_SHAPE, "batch (%d) out of range", batch);
+  CHAIN_LAUNCH("k_dense_any", k_dense_any, dim3((rows + kDenseTile - 1) / kDenseTile, unsigned(ti)), dim3(256), 0,
+               static_cast<cudaStream_t>(stream), 0, a);
+  return ok();
+}
+
+}  // extern "C"

@@ -9,8 +9,9 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct as _struct
 from dataclasses import dataclass
-from typing import List, Optional, Sequence
+from typing import List, Optional, Sequence, Tuple
 
 import numpy as np
 
@@ -42,6 +43,8 @@ EXPORTS = [
     "dfssm_model_decode_q8", "dfssm_quantize_rows_int8", "dfssm_phase_timers",
     "dfssm_prefill_workspace_bytes", "dfssm_prefill_workspace_layout", "dfssm_layer_prefill",
     "dfssm_model_prefill", "dfssm_df_field_words", "dfssm_df_encode", "dfssm_df_decode",
+    "dfssm_conv_prompt", "dfssm_conv_token", "dfssm_scan_workspace_bytes", "dfssm_scan_prompt", "dfssm_scan_token",
+    "dfssm_gated_norm", "dfssm_dense_forward",
 ]
 
 
@@ -123,6 +126,14 @@ def lib() -> C.CDLL:
     L.dfssm_df_field_words.argtypes = [i]
     L.dfssm_df_encode.argtypes = [vp, i, i, vp, vp, vp, vp, vp]
     L.dfssm_df_decode.argtypes = [vp, vp, vp, i, i, vp, vp]
+    st = C.c_char_p                      # a packed struct (the parts of a layer, below)
+    L.dfssm_conv_prompt.argtypes = L.dfssm_conv_token.argtypes = [i, i, i, st, vp, vp, st, vp, st, vp]
+    L.dfssm_scan_workspace_bytes.argtypes = [st, i, i, i]
+    L.dfssm_scan_workspace_bytes.restype = sz
+    L.dfssm_scan_prompt.argtypes = [st, st, st, st, st, st, vp, st, vp, sz, vp]
+    L.dfssm_scan_token.argtypes = [st, st, st, st, st, st, vp, st, vp]
+    L.dfssm_gated_norm.argtypes = [i, i, i, st, st, vp, st, vp]
+    L.dfssm_dense_forward.argtypes = [i, i, i, vp, vp, i, st, st, st, vp]
     L.dfssm_last_error.restype = C.c_char_p
     L.dfssm_version.restype = C.c_int
     for name in EXPORTS:
@@ -431,3 +442,175 @@ def df_decode(cells, lo, span, rows, stream=None) -> None:
     R, n = rows.shape
     _check(lib().dfssm_df_decode(_ptr(cells), _ptr(lo), _ptr(span), C.c_int(R), C.c_int(n), _ptr(rows),
                                  _stream(stream)))
+
+
+# ------------------------------------------------------------------ the parts of a layer
+
+# Their small structs (dfssm_rows, dfssm_seqs, dfssm_scan) are packed in one go: a token's
+# calls take microseconds, and filling ctypes fields one by one would be most of that.
+_ROWS = _struct.Struct("@Pqi4x").pack
+_SEQS = _struct.Struct("@iii4xPPPP").pack
+_SCAN = _struct.Struct("@iiiii4xPPP").pack
+_TYPES = {}
+
+
+def _types():
+    import torch
+    _TYPES.update({torch.float16: DTYPE_F16, torch.float32: DTYPE_F32})
+    return _TYPES
+
+
+def _rows(t, name: str, n: int, width: int) -> bytes:
+    """dfssm_rows of a 2-D tensor view [n, width] whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{n}, {width}] with contiguous rows, not {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
+    dtype = (_TYPES or _types()).get(t.dtype)
+    if dtype is None:
+        raise ValueError(f"{name}: {t.dtype} is neither float16 nor float32")
+    return _ROWS(t.data_ptr(), max(t.stride(0), width) if n <= 1 else t.stride(0), dtype)
+
+
+def _at(t, name: str, dtype, *shape) -> int:
+    """Address of a contiguous tensor of this type and shape; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, not {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _seqs(n_rows: int, start, slot, fresh, status, slots: int) -> bytes:
+    import torch
+    i32 = torch.int32
+    n = n_rows if start is None else start.shape[0] - 1
+    if n < 0:
+        raise ValueError("start must hold one more entry than there are sequences")
+    return _SEQS(n, n_rows, slots, _at(start, "start", i32, n + 1), _at(slot, "slot", i32, n),
+                 _at(fresh, "fresh", i32, n), 0 if status is None else _at(status, "status", i32, 1))
+
+
+def _call(fn, tensors, stream, *args) -> None:
+    """fn(*args, stream) on the device that all the tensors lie on."""
+    import torch
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError("all tensors must lie on one CUDA device")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, tensors, stream, *args)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    rc = fn(*args, raw)
+    if rc != OK:
+        raise DfssmError(rc, last_error())
+
+
+def _conv(fn, x, w, b, state, y, start, slot, fresh, silu, status, stream) -> None:
+    import torch
+    n, c = x.shape
+    width = w.shape[1]
+    slots = 0 if state is None else state.shape[0]
+    _call(fn, (x, w, b, state, y, start, slot, fresh, status), stream, c, width, int(silu), _rows(x, "x", n, c),
+          _at(w, "w", torch.float16, c, width), _at(b, "b", torch.float16, c),
+          _seqs(n, start, slot, fresh, status, slots), _at(state, "state", torch.float32, slots, width - 1, c),
+          _rows(y, "y", n, c))
+
+
+def conv_prompt(x, w, b, state, y, start, slot=None, fresh=None, silu=True, status=None, stream=None) -> None:
+    """Causal conv over packed prompts (dfssm_conv_prompt): x, y [rows, channels] (fp16 or
+    fp32, rows may be strided), w fp16 [channels, d_conv], b fp16 [channels] or None, state
+    fp32 [slots, d_conv - 1, channels] or None, start int32 [seqs + 1], slot and fresh
+    int32 [seqs] or None, status int32 [1] or None."""
+    _conv(lib().dfssm_conv_prompt, x, w, b, state, y, start, slot, fresh, silu, status, stream)
+
+
+def conv_token(x, w, b, state, y, slot=None, fresh=None, silu=True, status=None, stream=None) -> None:
+    """One conv step of every sequence (dfssm_conv_token); arguments as conv_prompt's."""
+    _conv(lib().dfssm_conv_token, x, w, b, state, y, None, slot, fresh, silu, status, stream)
+
+
+def _scan_struct(x, B, dt_bias, A_log, D, state, headdim, groups) -> Tuple[bytes, int, int]:
+    import torch
+    H = dt_bias.shape[0]
+    if state is not None:
+        P, N = state.shape[2], state.shape[3]
+        groups = B.shape[1] // max(N, 1)
+    elif headdim and groups:
+        P, N = headdim, B.shape[1] // groups
+    else:
+        raise ValueError("without a state, headdim and groups must be given")
+    f32 = torch.float32
+    return _SCAN(H, P, N, groups, DTYPE_F16 if state is not None and state.dtype == torch.float16 else DTYPE_F32,
+                 _at(dt_bias, "dt_bias", f32, H), _at(A_log, "A_log", f32, H), _at(D, "D", f32, H)), H * P, groups * N
+
+
+def scan_workspace_bytes(nheads: int, headdim: int, d_state: int, groups: int, n_seqs: int, n_rows: int,
+                         half: bool = False) -> int:
+    s = _SCAN(nheads, headdim, d_state, groups, DTYPE_F32, 0, 0, 0)
+    n = int(lib().dfssm_scan_workspace_bytes(s, DTYPE_F16 if half else DTYPE_F32, n_seqs, n_rows))
+    if n == 0:
+        raise DfssmError(ERR_INVALID_ARG, last_error())
+    return n
+
+
+def scan_workspace(x, state, n_seqs: int, groups: int = 1):
+    """Workspace tensor for scan_prompt on rows like x with states like state."""
+    import torch
+    n = scan_workspace_bytes(state.shape[1], state.shape[2], state.shape[3], groups, n_seqs, x.shape[0],
+                             x.dtype == torch.float16)
+    return torch.empty(n, dtype=torch.uint8, device=x.device)
+
+
+def _scan(fn, x, dt, B, Cm, dt_bias, A_log, D, state, y, start, slot, fresh, status, stream, ws, headdim, groups):
+    n = x.shape[0]
+    s, E, GN = _scan_struct(x, B, dt_bias, A_log, D, state, headdim, groups)
+    slots = 0
+    if state is not None:
+        slots = state.shape[0]
+        if not state.is_contiguous() or state.dtype not in (_TYPES or _types()) or state.shape[1] != dt_bias.shape[0]:
+            raise ValueError("state must be a contiguous fp32 or fp16 tensor [slots, heads, headdim, d_state]")
+    args = (s, _rows(x, "x", n, E), _rows(dt, "dt", n, dt_bias.shape[0]), _rows(B, "B", n, GN), _rows(Cm, "C", n, GN),
+            _seqs(n, start, slot, fresh, status, slots), _ptr(state), _rows(y, "y", n, E))
+    if ws is not None:
+        args += (ws.data_ptr(), ws.numel() * ws.element_size())
+    _call(fn, (x, dt, B, Cm, dt_bias, A_log, D, state, y, start, slot, fresh, status, ws), stream, *args)
+
+
+def scan_prompt(x, dt, B, C, dt_bias, A_log, D, state, y, start, ws, slot=None, fresh=None, status=None, stream=None,
+                headdim=None, groups=None) -> None:
+    """Selective scan over packed prompts (dfssm_scan_prompt): x, y [rows, heads * headdim],
+    B, C [rows, groups * d_state], dt [rows, heads] before bias and softplus (fp16 or fp32, rows
+    may be strided), dt_bias, A_log, D fp32 [heads] (D may be None), state fp32 or fp16
+    [slots, heads, headdim, d_state] or None (then headdim and groups say the shape), ws from
+    scan_workspace; start, slot, fresh, status as conv_prompt's."""
+    _scan(lib().dfssm_scan_prompt, x, dt, B, C, dt_bias, A_log, D, state, y, start, slot, fresh, status, stream, ws,
+          headdim, groups)
+
+
+def scan_token(x, dt, B, C, dt_bias, A_log, D, state, y, slot=None, fresh=None, status=None, stream=None) -> None:
+    """One scan step of every sequence (dfssm_scan_token); arguments as scan_prompt's."""
+    _scan(lib().dfssm_scan_token, x, dt, B, C, dt_bias, A_log, D, state, y, None, slot, fresh, status, stream, None,
+          None, None)
+
+
+def gated_norm(y, z, w, out, groups: int = 1, stream=None) -> None:
+    """out = rmsnorm(y * silu(z)) * w over each of `groups` parts of a row (dfssm_gated_norm);
+    z None: no gate.  y, z, out [rows, cols] fp16 or fp32, w fp16 [cols]."""
+    import torch
+    n, c = y.shape
+    _call(lib().dfssm_gated_norm, (y, z, w, out), stream, n, c, groups, _rows(y, "y", n, c),
+          None if z is None else _rows(z, "z", n, c), _at(w, "w", torch.float16, c), _rows(out, "out", n, c))
+
+
+def dense_forward(w, x, y, bias=None, residual=None, silu=False, stream=None) -> None:
+    """y = act(x w^T + bias) + residual (dfssm_dense_forward): w fp16 [rows, cols], x fp16
+    [batch, cols], bias fp16 [rows] or None, y and residual fp16 or fp32 [batch, rows]."""
+    import torch
+    rows, cols = w.shape
+    n = x.shape[0]
+    f16 = torch.float16
+    _call(lib().dfssm_dense_forward, (x, w, bias, residual, y), stream, rows, cols, n, _at(w, "w", f16, rows, cols),
+          _at(bias, "bias", f16, rows), int(silu), _rows(x, "x", n, cols),
+          None if residual is None else _rows(residual, "residual", n, rows), _rows(y, "y", n, rows))

@@ -368,6 +368,117 @@ DFSSM_API int dfssm_df_encode(const float* rows, int n_rows, int d_state, uint32
 DFSSM_API int dfssm_df_decode(const uint32_t* cells, const float* lo, const float* span, int n_rows,
                               int d_state, float* rows, void* stream);
 
+/* ---- the parts of a layer one by one: packed prompts and single tokens ------------
+ *
+ * The layer and model calls above take prompts of one length and one state per batch
+ * row.  A server packs prompts of different lengths one behind the other, keeps the
+ * states of many users in a pool of slots, and may hold layers whose projections are
+ * dense.  These calls are the parts such a layer is put together from, on the same
+ * weights, the same state layouts and the same formulas (Section 4.1; Section 2 for
+ * the chunked form of the scan; Appendix B, Table 12; RMSNorm eps 1e-5):
+ *
+ *   dfssm_gated_norm (pre-norm) -> dfssm_proj_forward or dfssm_dense_forward
+ *   -> dfssm_conv_prompt / _token -> dfssm_scan_prompt / _token
+ *   -> dfssm_gated_norm -> dfssm_proj_forward or dfssm_dense_forward
+ *
+ * Sums, running decays, norms and the states between tokens are held in 32 bits or
+ * more; outputs are rounded once, to the type of their rows.
+ *
+ * Rows.  A dfssm_rows is a matrix of activations: row i is a run of contiguous values
+ * at data + i * stride (stride in values, at least the row's length), fp16 or fp32, so
+ * that it may be a view of wider rows (x, B and C of the conv's output, z, xBC and dt
+ * of in_proj's).  data needs the alignment of its type only; 16-byte aligned rows take
+ * faster loads.  Output rows may not overlap any input, unless a call says so.
+ *
+ * Sequences.  n_seqs sequences lie in n_rows packed rows: sequence s is rows
+ * start[s] .. start[s + 1] - 1 (start: device int32 [n_seqs + 1], not decreasing, within
+ * [0, n_rows]).  Rows before start[0] and from start[n_seqs] on belong to no sequence.
+ * For single tokens start is NULL, n_rows == n_seqs and row s is sequence s.  Sequence s
+ * has its state in slot[s] (device int32 [n_seqs]; NULL: slot s) of a pool of n_slots
+ * states; where fresh (device int32 [n_seqs]; NULL: all zeros) is nonzero it begins from a
+ * zero state, whatever the slot holds; either way the slot receives the state after
+ * its last row.  A sequence of no rows leaves its slot as it was.  A sequence is left
+ * out -- its output rows and every slot stay as they were -- when its slot lies outside
+ * [0, n_slots) (a padded batch names -1), when an earlier sequence of the call names
+ * the same slot, or when its start or end breaks the rule above.  status (device uint32,
+ * may be NULL) then gets a bit or-ed in, never cleared: 1 slot >= n_slots or < -1, 2 the
+ * same slot twice, 4 a bad start (64: see the scan).  Output rows of no sequence stay as
+ * they were. */
+typedef struct dfssm_rows {
+  void* data;
+  int64_t stride;
+  int32_t dtype;      /* DFSSM_DTYPE_F16 or DFSSM_DTYPE_F32 */
+} dfssm_rows;
+
+typedef struct dfssm_seqs {
+  int32_t n_seqs, n_rows, n_slots;
+  const int32_t* start;
+  const int32_t* slot;
+  const int32_t* fresh;
+  uint32_t* status;
+} dfssm_seqs;
+
+/* Causal depthwise conv over each sequence (Section 4.1: the conv step as a stateful
+ * shift register):
+ *   y[t][c] = act(b[c] + sum_j w[c][j] x[t - (d_conv - 1) + j][c]),
+ * rows before the sequence's first coming from its state.  w fp16 [channels][d_conv],
+ * b fp16 [channels] or NULL, 2 <= d_conv <= 4, act SiLU (silu != 0) or none.
+ * conv_state fp32 [n_slots][d_conv - 1][channels], index 0 the oldest (the layout of
+ * dfssm_layer_state), updated in place; the prompt form takes NULL as well (every
+ * sequence begins from zeros, nothing is kept, slots are not looked at).  One launch. */
+DFSSM_API int dfssm_conv_prompt(int channels, int d_conv, int silu, const dfssm_rows* x, const uint16_t* w,
+                                const uint16_t* b, const dfssm_seqs* seqs, float* conv_state,
+                                const dfssm_rows* y, void* stream);
+DFSSM_API int dfssm_conv_token(int channels, int d_conv, int silu, const dfssm_rows* x, const uint16_t* w,
+                               const uint16_t* b, const dfssm_seqs* seqs, float* conv_state,
+                               const dfssm_rows* y, void* stream);
+
+/* Selective scan over each sequence (Appendix B, Table 12; Section 2).  Head h of group
+ * g = h / (nheads / ngroups), at row t:
+ *   dt = softplus(dt_raw[t][h] + dt_bias[h]),
+ *   state[h][p][n] = exp(-dt exp(A_log[h])) state[h][p][n] + dt x[t][h][p] B[t][g][n],
+ *   y[t][h][p] = sum_n C[t][g][n] state[h][p][n] + D[h] x[t][h][p].
+ * x, y rows of nheads * headdim, B, C rows of ngroups * d_state, dt rows of nheads; x, B
+ * and C share one type, dt and y have their own.  dt_bias, A_log, D fp32 [nheads] (D may be
+ * NULL: no such term).  state [n_slots][nheads][headdim][d_state], fp32 or fp16 (rounded
+ * once from 32 bits, after the last row), updated in place; the prompt form takes NULL
+ * as well (as the conv).  Limits: headdim a multiple of 16 and <= 128, d_state a multiple
+ * of 4 and <= 256, nheads a multiple of ngroups.  The token form is one launch and needs
+ * no workspace; the prompt form takes dfssm_scan_workspace_bytes bytes, not
+ * initialised, not shared by calls that may overlap.  A wait inside the prompt form that
+ * gives up (never seen) sets status bit 64; the outputs are then invalid. */
+typedef struct dfssm_scan {
+  int32_t nheads, headdim, d_state, ngroups;
+  int32_t state_dtype;      /* DFSSM_DTYPE_F32 or DFSSM_DTYPE_F16 */
+  const float* dt_bias;
+  const float* A_log;
+  const float* D;
+} dfssm_scan;
+
+DFSSM_API size_t dfssm_scan_workspace_bytes(const dfssm_scan* s, int dtype, int n_seqs, int n_rows);
+DFSSM_API int dfssm_scan_prompt(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* dt,
+                                const dfssm_rows* B, const dfssm_rows* C, const dfssm_seqs* seqs, void* state,
+                                const dfssm_rows* y, void* ws, size_t ws_bytes, void* stream);
+DFSSM_API int dfssm_scan_token(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* dt,
+                               const dfssm_rows* B, const dfssm_rows* C, const dfssm_seqs* seqs, void* state,
+                               const dfssm_rows* y, void* stream);
+
+/* Gated RMSNorm (Appendix B, Table 12: the gate before the norm) over each of ngroups
+ * equal parts of a row:  g = y silu(z), out = g rsqrt(mean(g^2) + 1e-5) w.  z NULL: no gate
+ * (a plain RMSNorm).  w fp16 [cols].  out may be the rows of y or of z themselves. */
+DFSSM_API int dfssm_gated_norm(int rows, int cols, int ngroups, const dfssm_rows* y, const dfssm_rows* z,
+                               const uint16_t* w, const dfssm_rows* out, void* stream);
+
+/* Dense projection for layers that keep fp16 weights:
+ *   y[i][o] = act(sum_k w[o][k] x[i][k] + b[o]) + residual[i][o],
+ * w fp16 [rows][cols] contiguous, x fp16 rows of cols, b fp16 [rows] or NULL, act SiLU (silu != 0)
+ * or none, residual NULL or rows of `rows` values, which may be y's own.  The sums are
+ * held in 32 bits.  w 16-byte aligned; cols a multiple of 8 and x rows 16-byte aligned
+ * take the tensor cores. */
+DFSSM_API int dfssm_dense_forward(int rows, int cols, int batch, const uint16_t* w, const uint16_t* b, int silu,
+                                  const dfssm_rows* x, const dfssm_rows* residual, const dfssm_rows* y,
+                                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif
