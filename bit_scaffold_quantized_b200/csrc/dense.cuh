@@ -1,0 +1,505 @@
+// Dense projection y = act(x w^T + b) + residual.
+//
+//   k_dense_tc    tcgen05.mma kind::f16 with fp32 accumulators in tensor memory: an M =
+//                 128 tile of weight rows against N = 16 .. 256 rows of x (so that a thread,
+//                 which owns a TMEM lane, owns a weight row, and a warp's stores of one x
+//                 row are 32 consecutive values);
+//   k_dense_any   rows that TMA cannot address (cols not a multiple of 8, or rows of x not
+//                 16-byte aligned).
+#pragma once
+
+#include <type_traits>
+
+#include "mixer.cuh"
+#include "tcgen05.cuh"
+
+namespace dfssm {
+
+struct DenseArgs {
+  int rows, cols, batch, silu, y16, r16;
+  const uint16_t* b;
+  const __half* w;
+  Rows x, r, y;
+  unsigned* status;
+  int n, tiles_m, tiles, stages;      // k_dense_tc: x rows per tile, tiles of weight rows, tiles in all
+};
+
+constexpr unsigned kStatusWait = 64u;      // a bounded wait gave up
+
+DFSSM_DEV float dense_residual(const DenseArgs& a, int i, int o) {
+  const long long at = i * a.r.stride + o;
+  return a.r16 ? __half2float(static_cast<const __half*>(a.r.p)[at]) : static_cast<const float*>(a.r.p)[at];
+}
+DFSSM_DEV void dense_store(const DenseArgs& a, int i, int o, float v) {
+  const long long at = i * a.y.stride + o;
+  if (a.y16) static_cast<__half*>(a.y.p)[at] = __float2half_rn(v);
+  else static_cast<float*>(a.y.p)[at] = v;
+}
+
+// Bias, activation, residual and stores of one weight row o for NC consecutive rows i0 ..
+// of x, of which n exist (n >= 1; o < a.rows).  The residual's loads go out together: y may
+// be the residual itself, so the compiler may not move a load over a store.
+template <typename TY, typename TR, int NC>
+DFSSM_DEV void dense_finish(const DenseArgs& a, const float (&acc)[NC], int i0, int o, int n, float bias) {
+  float res[NC];
+  if constexpr (!std::is_void_v<TR>) {
+    const TR* rp = static_cast<const TR*>(a.r.p) + o;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) res[i] = ldf(rp + (long long)(i0 + min(i, n - 1)) * a.r.stride);
+  }
+  TY* yp = static_cast<TY*>(a.y.p) + o;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    float v = acc[i] + bias;
+    if (a.silu) v = silu_f(v);
+    if constexpr (!std::is_void_v<TR>) v += res[i];
+    if (i < n) stf(yp + (long long)(i0 + i) * a.y.stride, v);
+  }
+}
+
+constexpr int kDenseTile = 64, kDenseK = 16;
+
+// 64 x 64 outputs per block, 4 x 4 per thread, fp32 FMA.
+__global__ void __launch_bounds__(256) k_dense_any(DenseArgs a) {
+  pdl_wait();
+  pdl_release();
+  __shared__ float xs[kDenseK][kDenseTile + 4], ws[kDenseK][kDenseTile + 4];
+  const int tid = threadIdx.x, o0 = blockIdx.x * kDenseTile, i0 = blockIdx.y * kDenseTile;
+  const int to = 4 * (tid & 15), ti = 4 * (tid >> 4);
+  const __half* xp = static_cast<const __half*>(a.x.p);
+  float acc[4][4] = {};
+  for (int k0 = 0; k0 < a.cols; k0 += kDenseK) {
+    __syncthreads();
+    for (int i = tid; i < kDenseTile * kDenseK; i += 256) {
+      const int r = i / kDenseK, k = i % kDenseK;
+      const bool kv = k0 + k < a.cols;
+      xs[k][r] = kv && i0 + r < a.batch ? __half2float(xp[(long long)(i0 + r) * a.x.stride + k0 + k]) : 0.f;
+      ws[k][r] = kv && o0 + r < a.rows ? __half2float(a.w[(long long)(o0 + r) * a.cols + k0 + k]) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kDenseK; ++k)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) acc[m][n] = fmaf(xs[k][ti + m], ws[k][to + n], acc[m][n]);
+  }
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int i = i0 + ti + m, o = o0 + to + n;
+      if (i >= a.batch || o >= a.rows) continue;
+      float v = acc[m][n] + (a.b ? h2f(a.b[o]) : 0.f);
+      if (a.silu) v = silu_f(v);
+      if (a.r.p) v += dense_residual(a, i, o);
+      dense_store(a, i, o, v);
+    }
+}
+
+// ---- few rows of x
+
+// Up to 8 NT rows of x: reading the weights once is all of the work, so that they go
+// straight from global memory into mma.sync fragments.  A block has 16 weight rows; its
+// warps share K, each with 32 columns at a time: lane (g, t) reads columns
+// 8 t .. 8 t + 7 of rows g and g + 8 in one 16-byte load each and the same columns of x row g of
+// every octet; the columns of a K = 16 product may come in any order if both sides use
+// the same, and product j takes columns 8 t + 4 j .. + 3.  At most eight products make a chain (see
+// k_dense_tc); the warps' totals meet in shared memory.
+
+__host__ __device__ constexpr size_t df_smem_bytes(int nt, int warps) {
+  return size_t(4) * warps * 8 * nt * (16 + 4);
+}
+
+template <typename TY, typename TR, int NT>
+__global__ void __launch_bounds__(512, NT <= 2 ? 2 : 1) k_dense_few(DenseArgs a) {
+  pdl_wait();
+  pdl_release();
+  extern __shared__ __align__(16) float df_red[];      // [warps][8 NT][20]
+  constexpr int R = 16, RS = R + 4, NC = 8 * NT;
+  constexpr int U = 4;                                 // 32-column pieces at a time; 2 U products make a chain
+  const int tid = threadIdx.x, warp = tid >> 5, warps = blockDim.x >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int o0 = blockIdx.x * R, i0 = blockIdx.y * NC;
+  const int blocks = (a.cols + 31) / 32, kb0 = blocks * warp / warps, kb1 = blocks * (warp + 1) / warps;
+  const __half* wp[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) wp[m] = a.w + (long long)min(o0 + 8 * m + g, a.rows - 1) * a.cols + 8 * t;
+  const __half* xp[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    xp[n] = static_cast<const __half*>(a.x.p) + (long long)min(i0 + 8 * n + g, a.batch - 1) * a.x.stride + 8 * t;
+  auto load_w = [&](int kb, uint4 (&v)[U][2]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const bool in = kb + u < kb1 && 32 * (kb + u) + 8 * t < a.cols;
+        v[u][m] = in ? __ldg(reinterpret_cast<const uint4*>(wp[m] + 32 * (kb + u))) : make_uint4(0, 0, 0, 0);
+      }
+  };
+  float total[NT][4] = {};
+  for (int kb = kb0; kb < kb1; kb += U) {
+    uint4 w[U][2];
+    load_w(kb, w);
+    float acc[NT][4] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = kb + u < kb1 && 32 * (kb + u) + 8 * t < a.cols;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(xp[n] + 32 * (kb + u))) : make_uint4(0, 0, 0, 0);
+        const uint4 p = w[u][0], q = w[u][1];
+        const uint32_t a0[4] = {p.x, q.x, p.y, q.y}, a1[4] = {p.z, q.z, p.w, q.w};
+        mma_f16_16816(acc[n], a0, x.x, x.y);
+        mma_f16_16816(acc[n], a1, x.z, x.w);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[n][i] += acc[n][i];
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) df_red[(warp * NC + 8 * n + 2 * t + (i & 1)) * RS + g + 8 * (i >> 1)] = total[n][i];
+  __syncthreads();
+  // thread = one weight row, columns (tid / R), + threads / R, ...
+  const int r = tid % R, o = o0 + r, step = blockDim.x / R;
+  if (o >= a.rows) return;
+  const float bias = a.b ? h2f(a.b[o]) : 0.f;
+  for (int c = tid / R; c < NC && i0 + c < a.batch; c += step) {
+    const int i = i0 + c;
+    float v[1] = {0.f};
+    for (int z = 0; z < warps; ++z) v[0] += df_red[(z * NC + c) * RS + r];
+    dense_finish<TY, TR, 1>(a, v, i, o, 1, bias);
+  }
+}
+
+// ---- tcgen05
+
+constexpr int kDtM = 256;                   // weight rows of a tile: 128 in each CTA of a pair
+constexpr int kDtK = 64;                    // columns of a stage: one 128-byte swizzle row
+constexpr int kDtMaxN = 256;
+constexpr int kDtEpiWarps = 8;              // warps 0..7: lanes 32 (w mod 4), column half w / 4
+constexpr int kDtThreads = 32 * (kDtEpiWarps + 2);
+constexpr int kDtMaxStages = 10;
+constexpr int kDtChain = 8;                 // stages whose MMAs add up in tensor memory
+constexpr int kDtMaxSplit = 4;              // pairs of a cluster sharing K
+constexpr int kDtSplitMaxN = 128;
+constexpr size_t kDtSmemCap = 220 * 1024;
+
+// Per CTA of the pair: its 128 weight rows and half of the tile's n rows of x.
+__host__ __device__ constexpr int dt_stage_bytes(int n) { return (kDtM / 2 + n / 2) * kDtK * 2; }
+// The ring, and with a K split the sums that the other pairs send: [ks][n / ks][128].
+__host__ __device__ constexpr size_t dt_smem_bytes(int n, int stages, int ks) {
+  return 1024 + size_t(stages) * dt_stage_bytes(n) + (ks > 1 ? size_t(n) * (kDtM / 2) * 4 : 0);
+}
+
+// kind::f16: D fp32, A and B fp16, both K-major.
+DFSSM_DEV uint32_t umma_idesc_f16(int m, int n) {
+  return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+DFSSM_DEV void umma_f16_ss_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      :: "r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(uint32_t(acc)) : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs of the pair once the MMAs issued
+// before it have finished.
+DFSSM_DEV void tc_commit_pair(uint64_t* bar, unsigned ctas) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+      :: "r"(smem_u32(bar)), "h"(uint16_t(ctas)) : "memory");
+}
+// A tile load whose bytes count on a barrier of either CTA of the pair.
+DFSSM_DEV void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+DFSSM_DEV void mbar_expect_tx_at(uint32_t bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
+}
+DFSSM_DEV void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+// 16 columns of this warp's 32 TMEM lanes.
+DFSSM_DEV void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t q[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]),
+        "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(q[i]);
+}
+DFSSM_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+DFSSM_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+DFSSM_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Persistent pairs of CTAs (clusters of two) over tiles of 256 weight rows x n rows of x:
+// each CTA holds 128 of the weight rows and half of the x rows, the pair's MMAs read both
+// halves of x from both shared memories, so that a stage is read from L2 once per pair.
+//   warp 8    TMA producer of its CTA's halves, 64 columns of K a stage (128-byte
+//             swizzle); their bytes count on the first CTA's `full` barrier;
+//   warp 9    of the first CTA: MMA issuer, four K = 16 MMAs per stage, kDtChain stages into
+//             one of two accumulators in tensor memory; commits reach both CTAs;
+//   warps 0..7  add each finished accumulator to the tile's sums in registers, then bias,
+//             activation, residual and stores (thread = weight row).
+// The tensor cores add into fp32 accumulators without rounding to nearest, and a long
+// chain of such adds leans to one side; a chain ends after kDtChain stages (32 MMAs) and
+// its sum joins an fp32 total by ordinary adds, while the other accumulator fills.  Without
+// an activation the total begins as the residual, whose loads then run beside the first
+// chain; the tile ends in stores alone, and the next one's MMAs run on under them.
+// K split (gridDim.z = ks pairs of one cluster): each pair sums its share of K and sends
+// (st.async) column c to pair c / (n / ks), which adds the ks sums and finishes them.
+template <typename TY, typename TR>
+__global__ void __launch_bounds__(kDtThreads, 1)
+    k_dense_tc(DenseArgs a, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[kDtMaxStages], empty[kDtMaxStages], accf[2], acce[2], done, rbar;
+  __shared__ uint32_t tmem_s;
+  __shared__ int fail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int N = a.n, S = a.stages, rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int ks = gridDim.z, kz = blockIdx.z, kblocks = (a.cols + kDtK - 1) / kDtK;
+  const int kb0 = kblocks * kz / ks, nkb = kblocks * (kz + 1) / ks - kb0, chains = (nkb + kDtChain - 1) / kDtChain;
+  const int STAGE = dt_stage_bytes(N);
+  const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
+  float* rcv = reinterpret_cast<float*>(smem_raw + (sbase - raw) + size_t(S) * STAGE);
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(&tmem_s)), "n"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (tid == 256) {
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&tm_x)) : "memory");
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 2);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&accf[i], 1);
+      mbar_init(&acce[i], 2 * kDtEpiWarps);
+    }
+    mbar_init(&done, 1);
+    mbar_init(&rbar, 1);
+    fail = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (ks > 1) mbar_expect_tx(&rbar, unsigned(N * (kDtM / 2) * 4));
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();          // both CTAs' barriers and tensor memory are there
+  tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  pdl_wait();
+  pdl_release();
+  const uint32_t full0 = cluster_map(smem_u32(&full[0]), 2u * kz);      // the pair's first CTA's barriers
+  const unsigned both = 3u << (2 * kz);
+  // Warps 8 and 9 walk their loops whole, and one elected lane issues: in warp-uniform code
+  // the operands stay in uniform registers (with one lane in the loop alone, a stage's
+  // four MMAs took 800 cycles to issue).
+  if (warp == 8) {
+    {
+      int st = 0;
+      unsigned wrap = 0;         // parity of the ring's next round; the first finds it empty
+      bool go = true, filled = false;
+      const bool one = elect_one();
+      for (int tile = pair; go && tile < a.tiles; tile += pairs) {
+        const int m0 = (tile % a.tiles_m) * kDtM + rank * (kDtM / 2), n0 = (tile / a.tiles_m) * N + rank * (N / 2);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (filled && !__all_sync(0xffffffffu, tc_wait(&empty[st], wrap ^ 1u, a.status, &fail, kStatusWait))) {
+            go = false;
+            break;
+          }
+          const uint32_t sg = sbase + st * STAGE, bar = full0 + 8 * st;
+          if (one) {
+            mbar_expect_tx_at(bar, STAGE);
+            tma_load_2d_pair(sg, &tm_w, (kb0 + kb) * kDtK, m0, bar);
+            tma_load_2d_pair(sg + kDtM / 2 * kDtK * 2, &tm_x, (kb0 + kb) * kDtK, n0, bar);
+          }
+          if (++st == S) {
+            st = 0;
+            wrap ^= 1u;
+            filled = true;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (rank == 0) {
+      const uint32_t idesc = umma_idesc_f16(kDtM, N);
+      const bool one = elect_one();
+      const uint64_t desc0 = umma_desc_sw128(sbase);
+      int st = 0;
+      unsigned round = 0, ch = 0;
+      bool go = true;
+      for (int tile = pair; go && tile < a.tiles; tile += pairs) {
+        for (int k = 0; go && k < nkb; ++ch) {
+          const int buf = int(ch & 1u);
+          if (ch >= 2 && !__all_sync(0xffffffffu, tc_wait(&acce[buf], ((ch >> 1) & 1u) ^ 1u, a.status, &fail, kStatusWait))) {
+            go = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + uint32_t(buf * kDtMaxN);
+          const int end = min(nkb, k + kDtChain);
+          for (bool first = true; k < end; ++k) {
+            if (!__all_sync(0xffffffffu, tc_wait(&full[st], round, a.status, &fail, kStatusWait))) {
+              go = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = desc0 + uint64_t(unsigned(st * STAGE) >> 4), bd = ad + (kDtM / 2 * kDtK * 2 >> 4);
+            if (one) {
+#pragma unroll
+              for (int kk = 0; kk < kDtK / 16; ++kk)
+                umma_f16_ss_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0 || !first);
+              tc_commit_pair(&empty[st], both);
+            }
+            first = false;
+            if (++st == S) {
+              st = 0;
+              round ^= 1u;
+            }
+          }
+          if (one) tc_commit_pair(&accf[buf], both);
+        }
+      }
+      if (!go) {
+        // no copy may still be landing (their bytes count here) and no MMA still running
+        // when the pair leaves: each stage's barrier is given time to complete its phase
+        for (int j = 0; j < S; ++j) {
+          long long spins = 0;
+          while (!mbar_try_wait(&full[(st + j) % S], st + j < S ? round : round ^ 1u) && ++spins < kTcSpinLimit / 64) {
+          }
+        }
+        if (one) tc_commit_pair(&done, both);
+        long long spins = 0;
+        while (!mbar_try_wait(&done, 0u) && ++spins < kTcSpinLimit) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, half = warp >> 2;
+    const int hc = (N / 16 + 1) / 2 * 16;                     // columns of the first half
+    const int c0 = half * hc, nc = half ? N - hc : hc;        // this warp's columns
+    const uint32_t tl = tmem + (uint32_t(32 * quarter) << 16) + uint32_t(c0);
+    const int r = 32 * quarter + lane;
+    const uint32_t free0 = cluster_map(smem_u32(&acce[0]), 2u * kz), free1 = cluster_map(smem_u32(&acce[1]), 2u * kz);
+    const bool early = !std::is_void_v<TR> && !a.silu && ks == 1;
+    // the residual of weight row o, x rows n0 .., all loads on their way at once (y may be
+    // the residual itself: no load may wait behind a store)
+    auto residual = [&](auto use, int o, int n0) {
+      if constexpr (!std::is_void_v<TR>) {
+        const TR* rp = static_cast<const TR*>(a.r.p) + min(o, a.rows - 1);
+#pragma unroll
+        for (int j = 0; j < kDtMaxN / 32; ++j)
+          if (16 * j < nc)
+#pragma unroll
+            for (int i = 16 * j; i < 16 * j + 16; ++i) use(i, ldf(rp + (long long)min(n0 + i, a.batch - 1) * a.r.stride));
+      }
+    };
+    unsigned ch = 0;
+    bool go = true;
+    for (int tile = pair; go && tile < a.tiles; tile += pairs) {
+      const int o = (tile % a.tiles_m) * kDtM + rank * (kDtM / 2) + r, n0 = (tile / a.tiles_m) * N + c0;
+      float acc[kDtMaxN / 2];
+      const float bias = ks == 1 && a.b && o < a.rows ? h2f(a.b[o]) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kDtMaxN / 2; ++i) acc[i] = 0.f;
+      if (early) residual([&](int i, float v) { acc[i] = v; }, o, n0);
+#pragma unroll
+      for (int i = 0; i < kDtMaxN / 2; ++i) acc[i] += bias;
+      for (int c = 0; c < chains; ++c, ++ch) {
+        const int buf = int(ch & 1u);
+        go = __all_sync(0xffffffffu, tc_wait(&accf[buf], (ch >> 1) & 1u, a.status, &fail, kStatusWait));
+        if (!go) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < kDtMaxN / 32; ++j)
+          if (16 * j < nc) {
+            float v[16];
+            tmem_ld16(tl + uint32_t(buf * kDtMaxN + 16 * j), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[16 * j + i] += v[i];
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(buf ? free1 : free0);
+      }
+      if (!go) break;
+      if (ks > 1) {
+        const int cs = N / ks;
+        const uint32_t base = smem_u32(rcv), bar = smem_u32(&rbar);
+        int p = c0 / cs, at = c0 % cs;
+#pragma unroll
+        for (int j = 0; j < kDtSplitMaxN / 2; ++j)
+          if (j < nc) {
+            const uint32_t dst = cluster_map(base + uint32_t(((kz * cs + at) * (kDtM / 2) + r) * 4), unsigned(2 * p + rank));
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+                         :: "r"(dst), "r"(__float_as_uint(acc[j])), "r"(cluster_map(bar, unsigned(2 * p + rank))) : "memory");
+            if (++at == cs) {
+              at = 0;
+              ++p;
+            }
+          }
+      } else {
+        // one loop per step, guarded once per 16 columns: the unrolled code of the steps that
+        // a call does not take must not be fetched (it cost 5 us a call)
+        if (a.silu) {
+#pragma unroll
+          for (int j = 0; j < kDtMaxN / 32; ++j)
+            if (16 * j < nc)
+#pragma unroll
+              for (int i = 16 * j; i < 16 * j + 16; ++i) acc[i] = silu_f(acc[i]);
+          residual([&](int i, float v) { acc[i] += v; }, o, n0);
+        }
+        if (o < a.rows) {
+          TY* yp = static_cast<TY*>(a.y.p) + o;
+#pragma unroll
+          for (int j = 0; j < kDtMaxN / 32; ++j)
+            if (16 * j < nc)
+#pragma unroll
+              for (int i = 16 * j; i < 16 * j + 16; ++i)
+                if (n0 + i < a.batch) stf(yp + (long long)(n0 + i) * a.y.stride, acc[i]);
+        }
+      }
+    }
+    if (ks > 1) {
+      // this CTA's n / ks columns: thread = (weight row, eight columns)
+      const int cs = N / ks, row = tid & 127;
+      const int o = (pair % a.tiles_m) * kDtM + rank * (kDtM / 2) + row;
+      const bool got = go && tc_wait(&rbar, 0u, a.status, &fail, kStatusWait);
+      if (got && o < a.rows) {
+        const float bias = a.b ? h2f(a.b[o]) : 0.f;
+        for (int c = 8 * (tid >> 7); c < cs; c += 16) {
+          const int i0 = (pair / a.tiles_m) * N + kz * cs + c, n = min(min(8, cs - c), a.batch - i0);
+          if (n <= 0) break;
+          float v[8] = {};
+          for (int z = 0; z < ks; ++z)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < n) v[i] += rcv[(z * cs + c + i) * (kDtM / 2) + row];
+          dense_finish<TY, TR, 8>(a, v, i0, o, n, bias);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();          // no CTA's shared or tensor memory is in use by another
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(512) : "memory");
+}
+
+}  // namespace dfssm

@@ -309,7 +309,7 @@ int launch_proj_tc_bg(const ProjArgs& a, cudaStream_t st) {
   if (int rc = proj_tc_maps(a, BG, &tb, &tp)) return rc;
   const int mt = (a.rows + kTcM - 1) / kTcM, gb = (a.batch + BG - 1) / BG;
   const int ks = proj_tc_split(mt * gb, a.K / kTileCols);
-  CHAIN_LAUNCH("k_proj_tc", k_proj_tc<EPI, BG>, dim3(mt, gb, ks), dim3(kTcThreads), size_t(smem), st, unsigned(ks),
+  CHAIN_LAUNCH("k_proj_tc", k_proj_tc<EPI, BG>, dim3(mt, gb, ks), dim3(kTcThreads), size_t(smem), st, dim3(1, 1, ks),
                a, tb, tp);
   return DFSSM_OK;
 }

@@ -726,62 +726,4 @@ __global__ void __launch_bounds__(kNormThreads) k_gated_norm_long(NormArgs a) {
   }
 }
 
-// ------------------------------------------------------------------ dense projection
-
-struct DenseArgs {
-  int rows, cols, batch, silu, y16, r16;
-  const uint16_t* w;
-  const uint16_t* b;
-  Rows x, r, y;
-};
-
-// The epilogue of one output: bias, activation, residual, store.
-DFSSM_DEV void dense_store(const DenseArgs& a, int i, int o, float v, float bias) {
-  v += bias;
-  if (a.silu) v = silu_f(v);
-  if (a.r.p) {
-    const long long at = i * a.r.stride + o;
-    v += a.r16 ? __half2float(static_cast<const __half*>(a.r.p)[at]) : static_cast<const float*>(a.r.p)[at];
-  }
-  const long long at = i * a.y.stride + o;
-  if (a.y16) static_cast<__half*>(a.y.p)[at] = __float2half_rn(v);
-  else static_cast<float*>(a.y.p)[at] = v;
-}
-
-constexpr int kDenseTile = 64, kDenseK = 16;
-
-// Any alignment: 64 x 64 outputs per block, 4 x 4 per thread, fp32 FMA.
-__global__ void __launch_bounds__(256) k_dense_any(DenseArgs a) {
-  pdl_wait();
-  pdl_release();
-  __shared__ float xs[kDenseK][kDenseTile + 4], ws[kDenseK][kDenseTile + 4];
-  const int tid = threadIdx.x, o0 = blockIdx.x * kDenseTile, i0 = blockIdx.y * kDenseTile;
-  const int to = 4 * (tid & 15), ti = 4 * (tid >> 4);
-  const __half* xp = static_cast<const __half*>(a.x.p);
-  const __half* wp = reinterpret_cast<const __half*>(a.w);
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < a.cols; k0 += kDenseK) {
-    __syncthreads();
-    for (int i = tid; i < kDenseTile * kDenseK; i += 256) {
-      const int r = i / kDenseK, k = i % kDenseK;
-      const bool kv = k0 + k < a.cols;
-      xs[k][r] = kv && i0 + r < a.batch ? __half2float(xp[(long long)(i0 + r) * a.x.stride + k0 + k]) : 0.f;
-      ws[k][r] = kv && o0 + r < a.rows ? __half2float(wp[(long long)(o0 + r) * a.cols + k0 + k]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kDenseK; ++k)
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) acc[m][n] = fmaf(xs[k][ti + m], ws[k][to + n], acc[m][n]);
-  }
-#pragma unroll
-  for (int m = 0; m < 4; ++m)
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-      if (i0 + ti + m < a.batch && o0 + to + n < a.rows)
-        dense_store(a, i0 + ti + m, o0 + to + n, acc[m][n], a.b ? h2f(a.b[o0 + to + n]) : 0.f);
-}
-
 }  // namespace dfssm

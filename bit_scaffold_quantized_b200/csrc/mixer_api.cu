@@ -4,6 +4,7 @@
 #include <climits>
 #include <cstring>
 
+#include "dense.cuh"
 #include "dfssm.h"
 #include "host.cuh"
 #include "mixer.cuh"
@@ -246,6 +247,139 @@ int norm_launch(const NormArgs& a, bool vec, cudaStream_t st) {
   return go(k_gated_norm_long<TY, TZ, TO>, kNormThreads);
 }
 
+// ---- dense
+
+// Rows of x per tile of k_dense_tc and its K split: the cheapest by a count of cycles.  A
+// stage of 64 columns costs the larger of its MMAs (2 n) and each CTA's (128 + n / 2)
+// 128-byte rows at the 40 bytes per cycle that an SM gets from L2 when all ask; a tile
+// costs its epilogue on top, a K split the exchange of the sums; tiles run in waves over
+// the pairs of SMs.
+struct DenseTile {
+  int n, ks;
+};
+
+// Clusters of ks pairs that can be resident at once (cached per device): an SM's GPC
+// must hold a whole cluster, so that larger ones leave more SMs over.
+int dense_clusters(int ks) {
+  static std::mutex mu;
+  static std::vector<std::array<int, 3>> cache;   // device, ks, clusters
+  const int dev = current_device();
+  std::lock_guard<std::mutex> lock(mu);
+  for (const auto& c : cache)
+    if (c[0] == dev && c[1] == ks) return c[2];
+  int n = 0;
+  const auto kernel = k_dense_tc<float, void>;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = unsigned(ks);
+  cfg.gridDim = dim3(2, 1, ks);
+  cfg.blockDim = dim3(kDtThreads);
+  cfg.dynamicSmemBytes = kDtSmemCap;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kDtSmemCap)) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = std::max(1, sm_count() / (2 * ks));
+  }
+  cache.push_back({dev, ks, n});
+  return n;
+}
+
+DenseTile dense_tile(int rows, int cols, int batch) {
+  DenseTile best{16, 1};
+  double cheapest = 0;
+  const int kblocks = (cols + kDtK - 1) / kDtK, tm = (rows + kDtM - 1) / kDtM;
+  for (int n = 16; n <= kDtMaxN; n += 16) {
+    const long long tiles = (long long)tm * ((batch + n - 1) / n);
+    for (int ks = 1; ks <= kDtMaxSplit; ks *= 2) {
+      const int room = dense_clusters(ks);
+      if (ks > 1 && (n > kDtSplitMaxN || tiles > room || kblocks < 2 * ks)) break;
+      const double stage = std::max(2.0 * n, 3.2 * (kDtM / 2 + n / 2));
+      const double cost = double((tiles + room - 1) / room) * ((kblocks + ks - 1) / ks * stage + 10.0 * n + 500.0) +
+                          (ks > 1 ? 1500.0 + 20.0 * n : 0.0);
+      if (cheapest == 0 || cost < cheapest) {
+        cheapest = cost;
+        best = DenseTile{n, ks};
+      }
+    }
+    if (n >= batch) break;
+  }
+  return best;
+}
+
+int dense_map(CUtensorMap* map, const void* p, long long cols, long long rows, long long stride, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(DFSSM_ERR_CUDA, "k_dense_tc: cuTensorMapEncodeTiled is not available");
+  const cuuint32_t estr[2] = {1, 1}, box[2] = {cuuint32_t(kDtK), cuuint32_t(box_rows)};
+  const cuuint64_t dim[2] = {cuuint64_t(cols), cuuint64_t(rows)}, str[1] = {cuuint64_t(stride) * 2};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(p), dim, str, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DFSSM_ERR_CUDA, "k_dense_tc: tensor map (%d)", int(r));
+  return DFSSM_OK;
+}
+
+// f(y type, residual type) of a dense call; void: no residual.
+template <typename F>
+int by_dense_types(const DenseArgs& a, F f) {
+  if (!a.r.p) return a.y16 ? f((__half*)nullptr, (void*)nullptr) : f((float*)nullptr, (void*)nullptr);
+  if (a.r16) return a.y16 ? f((__half*)nullptr, (__half*)nullptr) : f((float*)nullptr, (__half*)nullptr);
+  return a.y16 ? f((__half*)nullptr, (float*)nullptr) : f((float*)nullptr, (float*)nullptr);
+}
+
+int dense_tc(DenseArgs a, cudaStream_t st) {
+  const DenseTile t = dense_tile(a.rows, a.cols, a.batch);
+  a.n = t.n;
+  a.tiles_m = (a.rows + kDtM - 1) / kDtM;
+  const long long tiles = (long long)a.tiles_m * ((a.batch + a.n - 1) / a.n);
+  REQUIRE(tiles <= INT_MAX, DFSSM_ERR_UNSUPPORTED_SHAPE, "rows (%d) x batch (%d) out of range", a.rows, a.batch);
+  a.tiles = int(tiles);
+  a.stages = int(std::min<size_t>(kDtMaxStages, (kDtSmemCap - dt_smem_bytes(a.n, 0, t.ks)) / dt_stage_bytes(a.n)));
+  const size_t smem = dt_smem_bytes(a.n, a.stages, t.ks);
+  CUtensorMap tw, tx;
+  if (int rc = dense_map(&tw, a.w, a.cols, a.rows, a.cols, kDtM / 2)) return rc;
+  if (int rc = dense_map(&tx, a.x.p, a.cols, a.batch, a.x.stride, a.n / 2)) return rc;
+  const int pairs = std::min(a.tiles, dense_clusters(t.ks));
+  return by_dense_types(a, [&](auto* ty, auto* tr) {
+    const auto kernel = k_dense_tc<std::remove_pointer_t<decltype(ty)>, std::remove_pointer_t<decltype(tr)>>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return fail(DFSSM_ERR_CUDA, "k_dense_tc smem attribute: %s", cudaGetErrorString(e));
+    CHAIN_LAUNCH("k_dense_tc", kernel, dim3(2 * pairs, 1, t.ks), dim3(kDtThreads), smem, st, dim3(2, 1, t.ks), a, tw, tx);
+    return int(DFSSM_OK);
+  });
+}
+
+template <int NT>
+int dense_few(const DenseArgs& a, cudaStream_t st) {
+  const int gx = (a.rows + 15) / 16, gy = (a.batch + 8 * NT - 1) / (8 * NT);
+  // 16 warps share a long K where there are few blocks
+  const int warps = gx * gy <= 2 * sm_count() && a.cols >= 2048 ? 16 : 8;
+  const size_t smem = df_smem_bytes(NT, warps);
+  return by_dense_types(a, [&](auto* ty, auto* tr) {
+    const auto kernel = k_dense_few<std::remove_pointer_t<decltype(ty)>, std::remove_pointer_t<decltype(tr)>, NT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return fail(DFSSM_ERR_CUDA, "k_dense_few smem attribute: %s", cudaGetErrorString(e));
+    CHAIN_LAUNCH("k_dense_few", kernel, dim3(gx, gy), dim3(32 * warps), smem, st, 0, a);
+    return int(DFSSM_OK);
+  });
+}
+
+// Rows of x up to which k_dense_few runs.  Measured, us (k_dense_few / k_dense_tc): 8512 x
+// 2048 weights, 8 rows 7.7 / 12.7, 32 rows 13.4 / 13.6, 64 rows 27.4 / 14.0; 2048 x 4096, 8 rows
+// 6.1 / 10.5, 32 rows 8.1 / 11.1, 64 rows 31.6 / 11.6; 256 x 512, 32 rows 2.9 / 6.5.
+constexpr int kDenseFew = 32;
+
+int dense_aligned(const DenseArgs& a, cudaStream_t st) {
+  if (a.batch > kDenseFew) return dense_tc(a, st);
+  if (a.batch <= 8) return dense_few<1>(a, st);
+  if (a.batch <= 16) return dense_few<2>(a, st);
+  return dense_few<4>(a, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -344,7 +478,8 @@ int dfssm_gated_norm(int rows, int cols, int ngroups, const dfssm_rows* y, const
 }
 
 int dfssm_dense_forward(int rows, int cols, int batch, const uint16_t* w, const uint16_t* b, int silu,
-                        const dfssm_rows* x, const dfssm_rows* residual, const dfssm_rows* y, void* stream) {
+                        const dfssm_rows* x, const dfssm_rows* residual, const dfssm_rows* y, uint32_t* status,
+                        void* stream) {
   REQUIRE(rows > 0 && cols > 0 && batch >= 0, DFSSM_ERR_INVALID_ARG, "rows (%d), cols (%d) or batch (%d) out of range", rows,
           cols, batch);
   REQUIRE_PTR(w);
@@ -356,16 +491,21 @@ int dfssm_dense_forward(int rows, int cols, int batch, const uint16_t* w, const 
     REQUIRE(residual->data != y->data || (residual->dtype == y->dtype && residual->stride == y->stride),
             DFSSM_ERR_INVALID_ARG, "y shares its data with a residual of another dtype or stride");
   }
+  REQUIRE(reinterpret_cast<uintptr_t>(status) % 4 == 0, DFSSM_ERR_MISALIGNED, "status is not 4-byte aligned");
   if (batch == 0) return ok();
   DenseArgs a{};
-  a.rows = rows; a.cols = cols; a.batch = batch; a.silu = silu != 0;
-  a.w = w; a.b = b; a.x = dev_rows(x); a.r = dev_rows(residual); a.y = dev_rows(y);
+  a.rows = rows; a.cols = cols; a.batch = batch; a.silu = silu != 0; a.status = status;
+  a.w = reinterpret_cast<const __half*>(w); a.b = b; a.x = dev_rows(x); a.r = dev_rows(residual); a.y = dev_rows(y);
   a.y16 = y->dtype == DFSSM_DTYPE_F16;
   a.r16 = residual && residual->dtype == DFSSM_DTYPE_F16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cols % 8 == 0 && rows_in_pieces(x, 8)) {      // 16-byte loads and TMA
+    rc = dense_aligned(a, st);
+    return rc ? rc : ok();
+  }
   const long long ti = (batch + kDenseTile - 1) / kDenseTile;
   REQUIRE(ti <= 65535, DFSSM_ERR_UNSUPPORTED_SHAPE, "batch (%d) out of range", batch);
-  CHAIN_LAUNCH("k_dense_any", k_dense_any, dim3((rows + kDenseTile - 1) / kDenseTile, unsigned(ti)), dim3(256), 0,
-               static_cast<cudaStream_t>(stream), 0, a);
+  CHAIN_LAUNCH("k_dense_any", k_dense_any, dim3((rows + kDenseTile - 1) / kDenseTile, unsigned(ti)), dim3(256), 0, st, 0, a);
   return ok();
 }
 

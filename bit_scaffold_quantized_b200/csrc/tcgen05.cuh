@@ -17,17 +17,26 @@ DFSSM_DEV uint64_t umma_desc_sw128(uint32_t saddr) {
          (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+// One lane of a converged warp.
+DFSSM_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 DFSSM_DEV void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
 }
 
-DFSSM_DEV bool tc_wait(uint64_t* bar, unsigned parity, unsigned* status, int* fail) {
+// Bounded wait; one that gives up sets `bit` in *status and *fail, which ends the block's
+// other waits.
+DFSSM_DEV bool tc_wait(uint64_t* bar, unsigned parity, unsigned* status, int* fail, unsigned bit = 65536u) {
   long long spins = 0;
   while (!mbar_try_wait(bar, parity)) {
     if (++spins > kTcSpinLimit || *reinterpret_cast<volatile int*>(fail)) {
-      if (spins > kTcSpinLimit && status) atomicOr(status, 65536u);
+      if (spins > kTcSpinLimit && status) atomicOr(status, bit);
       *reinterpret_cast<volatile int*>(fail) = 1;
       return false;
     }

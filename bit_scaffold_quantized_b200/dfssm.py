@@ -133,7 +133,7 @@ def lib() -> C.CDLL:
     L.dfssm_scan_prompt.argtypes = [st, st, st, st, st, st, vp, st, vp, sz, vp]
     L.dfssm_scan_token.argtypes = [st, st, st, st, st, st, vp, st, vp]
     L.dfssm_gated_norm.argtypes = [i, i, i, st, st, vp, st, vp]
-    L.dfssm_dense_forward.argtypes = [i, i, i, vp, vp, i, st, st, st, vp]
+    L.dfssm_dense_forward.argtypes = [i, i, i, vp, vp, i, st, st, st, vp, vp]
     L.dfssm_last_error.restype = C.c_char_p
     L.dfssm_version.restype = C.c_int
     for name in EXPORTS:
@@ -604,13 +604,15 @@ def gated_norm(y, z, w, out, groups: int = 1, stream=None) -> None:
           None if z is None else _rows(z, "z", n, c), _at(w, "w", torch.float16, c), _rows(out, "out", n, c))
 
 
-def dense_forward(w, x, y, bias=None, residual=None, silu=False, stream=None) -> None:
+def dense_forward(w, x, y, bias=None, residual=None, silu=False, status=None, stream=None) -> None:
     """y = act(x w^T + bias) + residual (dfssm_dense_forward): w fp16 [rows, cols], x fp16
-    [batch, cols], bias fp16 [rows] or None, y and residual fp16 or fp32 [batch, rows]."""
+    [batch, cols], bias fp16 [rows] or None, y and residual fp16 or fp32 [batch, rows]; y may be the
+    residual itself."""
     import torch
     rows, cols = w.shape
     n = x.shape[0]
     f16 = torch.float16
-    _call(lib().dfssm_dense_forward, (x, w, bias, residual, y), stream, rows, cols, n, _at(w, "w", f16, rows, cols),
+    _call(lib().dfssm_dense_forward, (x, w, bias, residual, y, status), stream, rows, cols, n, _at(w, "w", f16, rows, cols),
           _at(bias, "bias", f16, rows), int(silu), _rows(x, "x", n, cols),
-          None if residual is None else _rows(residual, "residual", n, rows), _rows(y, "y", n, rows))
+          None if residual is None else _rows(residual, "residual", n, rows), _rows(y, "y", n, rows),
+          _at(status, "status", torch.int32, 1))

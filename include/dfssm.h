@@ -474,10 +474,11 @@ DFSSM_API int dfssm_gated_norm(int rows, int cols, int ngroups, const dfssm_rows
  * w fp16 [rows][cols] contiguous, x fp16 rows of cols, b fp16 [rows] or NULL, act SiLU (silu != 0)
  * or none, residual NULL or rows of `rows` values, which may be y's own.  The sums are
  * held in 32 bits.  w 16-byte aligned; cols a multiple of 8 and x rows 16-byte aligned
- * take the tensor cores. */
+ * take the tensor cores.  status (device uint32, may be NULL) gets bit 64 or-ed in if a wait
+ * inside gives up (never seen; y is then invalid). */
 DFSSM_API int dfssm_dense_forward(int rows, int cols, int batch, const uint16_t* w, const uint16_t* b, int silu,
                                   const dfssm_rows* x, const dfssm_rows* residual, const dfssm_rows* y,
-                                  void* stream);
+                                  uint32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

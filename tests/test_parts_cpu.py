@@ -134,8 +134,8 @@ def test_norm_and_dense_refusals():
     expect(SHAPE, norm(r=1 << 30, c=512, g=8), "out of range")
     assert norm(r=0) == 0
 
-    def dense(o=64, k=64, n=4, w=FAKE, b=FAKE, x=rows(dtype=F.DTYPE_F16), r=NULL, y=rows(ptr=2 * FAKE)):
-        return L.dfssm_dense_forward(o, k, n, w, b, 0, x, r, y, None)
+    def dense(o=64, k=64, n=4, w=FAKE, b=FAKE, x=rows(dtype=F.DTYPE_F16), r=NULL, y=rows(ptr=2 * FAKE), st=NULL):
+        return L.dfssm_dense_forward(o, k, n, w, b, 0, x, r, y, st, None)
     expect(INV, dense(o=0), "rows")
     expect(INV, dense(n=-1), "batch")
     expect(INV, dense(w=0), "w is NULL")
@@ -145,6 +145,7 @@ def test_norm_and_dense_refusals():
     expect(INV, dense(x=rows(dtype=F.DTYPE_F16, stride=63)), "x: stride")
     expect(INV, dense(r=rows(ptr=2 * FAKE, dtype=F.DTYPE_F16)), "shares")
     expect(INV, dense(r=rows(ptr=0)), "residual is NULL")
+    expect(MIS, dense(st=FAKE + 2), "status")
     assert dense(n=0) == 0
 
 
