@@ -24,8 +24,6 @@ struct DenseArgs {
   int n, tiles_m, tiles, stages;      // k_dense_tc: x rows per tile, tiles of weight rows, tiles in all
 };
 
-constexpr unsigned kStatusWait = 64u;      // a bounded wait gave up
-
 DFSSM_DEV float dense_residual(const DenseArgs& a, int i, int o) {
   const long long at = i * a.r.stride + o;
   return a.r16 ? __half2float(static_cast<const __half*>(a.r.p)[at]) : static_cast<const float*>(a.r.p)[at];
@@ -196,10 +194,6 @@ __host__ __device__ constexpr size_t dt_smem_bytes(int n, int stages, int ks) {
   return 1024 + size_t(stages) * dt_stage_bytes(n) + (ks > 1 ? size_t(n) * (kDtM / 2) * 4 : 0);
 }
 
-// kind::f16: D fp32, A and B fp16, both K-major.
-DFSSM_DEV uint32_t umma_idesc_f16(int m, int n) {
-  return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
-}
 DFSSM_DEV void umma_f16_ss_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
@@ -226,21 +220,6 @@ DFSSM_DEV void mbar_expect_tx_at(uint32_t bar, unsigned bytes) {
 DFSSM_DEV void mbar_arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
-// 16 columns of this warp's 32 TMEM lanes.
-DFSSM_DEV void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t q[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]),
-        "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(q[i]);
-}
-DFSSM_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-DFSSM_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-DFSSM_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
 // Persistent pairs of CTAs (clusters of two) over tiles of 256 weight rows x n rows of x:
 // each CTA holds 128 of the weight rows and half of the x rows, the pair's MMAs read both
 // halves of x from both shared memories, so that a stage is read from L2 once per pair.
@@ -314,7 +293,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       for (int tile = pair; go && tile < a.tiles; tile += pairs) {
         const int m0 = (tile % a.tiles_m) * kDtM + rank * (kDtM / 2), n0 = (tile / a.tiles_m) * N + rank * (N / 2);
         for (int kb = 0; kb < nkb; ++kb) {
-          if (filled && !__all_sync(0xffffffffu, tc_wait(&empty[st], wrap ^ 1u, a.status, &fail, kStatusWait))) {
+          if (filled && !__all_sync(0xffffffffu, tc_wait(&empty[st], wrap ^ 1u, a.status, &fail, kSeqWait))) {
             go = false;
             break;
           }
@@ -344,7 +323,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       for (int tile = pair; go && tile < a.tiles; tile += pairs) {
         for (int k = 0; go && k < nkb; ++ch) {
           const int buf = int(ch & 1u);
-          if (ch >= 2 && !__all_sync(0xffffffffu, tc_wait(&acce[buf], ((ch >> 1) & 1u) ^ 1u, a.status, &fail, kStatusWait))) {
+          if (ch >= 2 && !__all_sync(0xffffffffu, tc_wait(&acce[buf], ((ch >> 1) & 1u) ^ 1u, a.status, &fail, kSeqWait))) {
             go = false;
             break;
           }
@@ -352,7 +331,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           const uint32_t d = tmem + uint32_t(buf * kDtMaxN);
           const int end = min(nkb, k + kDtChain);
           for (bool first = true; k < end; ++k) {
-            if (!__all_sync(0xffffffffu, tc_wait(&full[st], round, a.status, &fail, kStatusWait))) {
+            if (!__all_sync(0xffffffffu, tc_wait(&full[st], round, a.status, &fail, kSeqWait))) {
               go = false;
               break;
             }
@@ -421,7 +400,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       for (int i = 0; i < kDtMaxN / 2; ++i) acc[i] += bias;
       for (int c = 0; c < chains; ++c, ++ch) {
         const int buf = int(ch & 1u);
-        go = __all_sync(0xffffffffu, tc_wait(&accf[buf], (ch >> 1) & 1u, a.status, &fail, kStatusWait));
+        go = __all_sync(0xffffffffu, tc_wait(&accf[buf], (ch >> 1) & 1u, a.status, &fail, kSeqWait));
         if (!go) break;
         tc_fence_after();
 #pragma unroll
@@ -479,7 +458,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       // this CTA's n / ks columns: thread = (weight row, eight columns)
       const int cs = N / ks, row = tid & 127;
       const int o = (pair % a.tiles_m) * kDtM + rank * (kDtM / 2) + row;
-      const bool got = go && tc_wait(&rbar, 0u, a.status, &fail, kStatusWait);
+      const bool got = go && tc_wait(&rbar, 0u, a.status, &fail, kSeqWait);
       if (got && o < a.rows) {
         const float bias = a.b ? h2f(a.b[o]) : 0.f;
         for (int c = 8 * (tid >> 7); c < cs; c += 16) {

@@ -21,6 +21,7 @@ struct Seqs {
 };
 
 constexpr unsigned kSeqBadSlot = 1u, kSeqSameSlot = 2u, kSeqBadStart = 4u;
+constexpr unsigned kSeqWait = 64u;       // a bounded wait gave up
 
 DFSSM_DEV float ldf(const float* p) { return *p; }
 DFSSM_DEV float ldf(const __half* p) { return __half2float(*p); }

@@ -8,6 +8,7 @@
 #include "dfssm.h"
 #include "host.cuh"
 #include "mixer.cuh"
+#include "scan_tc.cuh"
 
 using namespace dfssm;
 
@@ -136,19 +137,27 @@ int check_scan(const dfssm_scan* s) {
   return DFSSM_OK;
 }
 
-// Segments of the prompt form: enough (segment, head) blocks for about four per SM, and
-// no shorter than four chunks, below which the states between segments cost more to
-// move than the rows.
+// Whether the prompt form runs on the tensor cores (k_scan_tc): fp16 rows of heads of 64
+// with 64 or 128 states, heads in pairs of one group.  (The rows' alignment decides at the
+// call: the workspace is large enough for either.)
+bool scan_tc_shape(const dfssm_scan* s, int dtype) {
+  return dtype == DFSSM_DTYPE_F16 && s->headdim == kStP && (s->d_state == 64 || s->d_state == 128) &&
+         s->nheads / s->ngroups % 2 == 0;
+}
+
+// Segments of the prompt form: enough blocks for the SMs, and not much shorter than what
+// the states between segments cost to move.
 struct ScanPlan {
   int seg, max_segs;
   size_t decay_at, bytes;
 };
 
-ScanPlan scan_plan(const dfssm_scan* s, int n_seqs, int n_rows) {
+ScanPlan scan_plan(const dfssm_scan* s, bool tc, int n_seqs, int n_rows) {
   ScanPlan p;
-  const long long want = 4LL * sm_count();
-  long long seg = ((long long)n_rows * s->nheads + want - 1) / want;
-  seg = std::max<long long>(4 * kScanQ, (seg + kScanQ - 1) / kScanQ * kScanQ);
+  const int unit = tc ? kStQ : kScanQ, heads = tc ? s->nheads / 2 : s->nheads;
+  const long long want = tc ? 2LL * sm_count() : 4LL * sm_count();
+  long long seg = ((long long)n_rows * heads + want - 1) / want;
+  seg = std::max<long long>(tc ? 2 * kStQ : 4 * kScanQ, (seg + unit - 1) / unit * unit);
   if (seg >= n_rows) {
     p.seg = int(seg);
     p.max_segs = n_seqs;
@@ -222,6 +231,39 @@ int scan_prompt_launch(const ScanArgs& a, cudaStream_t st) {
     CHAIN_LAUNCH("k_scan_join", k_scan_join<TS>, dim3(a.q.n_seqs, a.H, (a.P * a.N + 1023) / 1024), dim3(256), 0, st, 0, a);
   }
   CHAIN_LAUNCH("k_scan_prompt", k_scan_prompt<TX, TY, TS, false>, grid, dim3(kScanThreads), smem, st, 0, a);
+  return DFSSM_OK;
+}
+
+int scan_map(CUtensorMap* map, const Rows& r, long long cols, int n_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(DFSSM_ERR_CUDA, "k_scan_tc: cuTensorMapEncodeTiled is not available");
+  const cuuint32_t estr[2] = {1, 1}, box[2] = {64, cuuint32_t(kStQ)};
+  const cuuint64_t dim[2] = {cuuint64_t(cols), cuuint64_t(n_rows)}, str[1] = {cuuint64_t(r.stride) * 2};
+  const CUresult e = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, r.p, dim, str, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (e != CUDA_SUCCESS) return fail(DFSSM_ERR_CUDA, "k_scan_tc: tensor map (%d)", int(e));
+  return DFSSM_OK;
+}
+
+template <typename TY, typename TS, int N>
+int scan_tc_launch(const ScanArgs& a, cudaStream_t st) {
+  CUtensorMap mx, mb, mc;
+  int rc;
+  if ((rc = scan_map(&mx, a.x, (long long)a.H * a.P, a.q.n_rows)) ||
+      (rc = scan_map(&mb, a.B, (long long)a.G * a.N, a.q.n_rows)) ||
+      (rc = scan_map(&mc, a.C, (long long)a.G * a.N, a.q.n_rows)))
+    return rc;
+  const dim3 grid(a.max_segs, a.H / 2);
+  constexpr size_t smem = st_smem_bytes(N, false), states = st_smem_bytes(N, true);
+  cudaError_t e = cudaFuncSetAttribute(k_scan_tc<TY, TS, N, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_scan_tc<float, TS, N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(states));
+  if (e != cudaSuccess) return fail(DFSSM_ERR_CUDA, "k_scan_tc smem attribute: %s", cudaGetErrorString(e));
+  if (a.seg_state) {
+    CHAIN_LAUNCH("k_scan_tc", k_scan_tc<float, TS, N, true>, grid, dim3(kStThreads), states, st, 0, a, mx, mb, mc);
+    CHAIN_LAUNCH("k_scan_join", k_scan_join<TS>, dim3(a.q.n_seqs, a.H, (a.P * a.N + 1023) / 1024), dim3(256), 0, st, 0, a);
+  }
+  CHAIN_LAUNCH("k_scan_tc", k_scan_tc<TY, TS, N, false>, grid, dim3(kStThreads), smem, st, 0, a, mx, mb, mc);
   return DFSSM_OK;
 }
 
@@ -401,7 +443,8 @@ size_t dfssm_scan_workspace_bytes(const dfssm_scan* s, int dtype, int n_seqs, in
     return 0;
   }
   ok();
-  return std::max<size_t>(16, scan_plan(s, n_seqs, n_rows).bytes);
+  const size_t any = scan_plan(s, false, n_seqs, n_rows).bytes;
+  return std::max<size_t>({16, any, scan_tc_shape(s, dtype) ? scan_plan(s, true, n_seqs, n_rows).bytes : 0});
 }
 
 int dfssm_scan_prompt(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* dt, const dfssm_rows* B,
@@ -414,7 +457,9 @@ int dfssm_scan_prompt(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows
   REQUIRE(ws_bytes >= need, DFSSM_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", ws_bytes, need);
   if (seqs->n_seqs == 0 || seqs->n_rows == 0) return ok();
   ScanArgs a = scan_args(s, x, dt, B, C, seqs, state, y);
-  const ScanPlan p = scan_plan(s, seqs->n_seqs, seqs->n_rows);
+  const bool tc = scan_tc_shape(s, x->dtype) && rows_in_pieces(x, 8) && rows_in_pieces(B, 8) && rows_in_pieces(C, 8) &&
+                  rows_in_pieces(y, 8);
+  const ScanPlan p = scan_plan(s, tc, seqs->n_seqs, seqs->n_rows);
   a.seg = p.seg;
   a.max_segs = p.max_segs;
   if (p.bytes) {
@@ -422,6 +467,14 @@ int dfssm_scan_prompt(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows
     a.seg_decay = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + p.decay_at);
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tc) {
+    rc = by_types(s->state_dtype, y->dtype, [&](auto ts, auto ty) {
+      using TS = decltype(ts);
+      using TY = decltype(ty);
+      return s->d_state == 64 ? scan_tc_launch<TY, TS, 64>(a, st) : scan_tc_launch<TY, TS, 128>(a, st);
+    });
+    return rc ? rc : ok();
+  }
   rc = by_types(x->dtype, y->dtype, [&](auto tx, auto ty) {
     using TX = decltype(tx);
     using TY = decltype(ty);

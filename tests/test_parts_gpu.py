@@ -157,7 +157,8 @@ def test_conv_pieces_equal_the_whole():
 # ------------------------------------------------------------------ scan
 
 SHAPES = [(8, 64, 16, 1), (4, 64, 128, 1), (3, 16, 4, 3), (6, 32, 20, 2), (2, 128, 256, 1), (5, 48, 200, 5),
-          (2, 96, 64, 1), (1, 64, 128, 1), (6, 64, 64, 2)]
+          (2, 96, 64, 1), (1, 64, 128, 1), (6, 64, 64, 2),
+          (8, 64, 64, 2), (4, 64, 128, 2)]
 
 
 def scan_case(rows, shape, xt, dtt, st, slots, seed, decay=16.0):
