@@ -333,11 +333,11 @@ struct ScanArgs {
   float* seg_decay;      // [max_segs][H]: decay over the segment
 };
 
-DFSSM_DEV float scan_dt(const ScanArgs& a, long long row, int h) {
+DFSSM_DEV float scan_raw(const ScanArgs& a, long long row, int h) {
   const long long at = row * a.dt.stride + h;
-  const float raw = a.dt16 ? __half2float(static_cast<const __half*>(a.dt.p)[at]) : static_cast<const float*>(a.dt.p)[at];
-  return softplus_f(raw + a.dt_bias[h]);
+  return a.dt16 ? __half2float(static_cast<const __half*>(a.dt.p)[at]) : static_cast<const float*>(a.dt.p)[at];
 }
+DFSSM_DEV float scan_dt(const ScanArgs& a, long long row, int h) { return softplus_f(scan_raw(a, row, h) + a.dt_bias[h]); }
 
 constexpr int kTokThreads = 128;
 
@@ -602,6 +602,8 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_prompt(ScanArgs a) {
   }
 }
 
+constexpr int kJoinAhead = 8;
+
 // The states between segments: thread = four values of one head's state of one sequence;
 // segment k's own state (from zero) gives way to the state that enters segment k.
 template <typename TS>
@@ -622,16 +624,25 @@ __global__ void __launch_bounds__(256) k_scan_join(ScanArgs a) {
   }
   if (i >= a.P * a.N) return;
   const int first = seg_first(a, s, b);
-  for (int k = 0; k < count; ++k) {
-    float* at = a.seg_state + (size_t(first + k) * a.H + h) * a.P * a.N + i;
-    float own[4] = {0.f, 0.f, 0.f, 0.f}, d = 0.f;
-    if (k + 1 < count) {
-      ldv<4>(at, own);
-      d = a.seg_decay[size_t(first + k) * a.H + h];
-    }
-    stv<4>(at, v);
+  const size_t step = size_t(a.H) * a.P * a.N;
+  float* at = a.seg_state + (size_t(first) * a.H + h) * a.P * a.N + i;
+  const float* dec = a.seg_decay + size_t(first) * a.H + h;
+  for (int k = 0; k < count; k += kJoinAhead) {       // several segments' loads at a time
+    float own[kJoinAhead][4], d[kJoinAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], d, own[j]);
+    for (int u = 0; u < kJoinAhead; ++u)
+      if (k + u + 1 < count) {
+        ldv<4>(at + (k + u) * step, own[u]);
+        d[u] = dec[size_t(k + u) * a.H];
+      }
+#pragma unroll
+    for (int u = 0; u < kJoinAhead; ++u)
+      if (k + u < count) {
+        stv<4>(at + (k + u) * step, v);
+        if (k + u + 1 < count)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], d[u], own[u][j]);
+      }
   }
 }
 

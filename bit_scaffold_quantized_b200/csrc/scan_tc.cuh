@@ -39,11 +39,13 @@ constexpr int kStThreads = 384;
 constexpr int kStP = 64;
 
 __host__ __device__ constexpr int st_tile_bytes(int n) { return kStQ * n * 2; }
-// Tables of a chunk and head: cs log2 e as hi and lo, dt, exp(cs), W's factors.
-constexpr int kStHi = 0, kStLo = kStQ, kStDt = 2 * kStQ, kStExp = 3 * kStQ, kStW = 4 * kStQ, kStTab = 5 * kStQ;
+// Tables of a chunk and head: cs log2 e as hi and lo, dt, exp(cs), W's factors, and
+// exp(cs_e - cs_s) dt_s with e the last row of the 32 that s belongs to.
+constexpr int kStHi = 0, kStLo = kStQ, kStDt = 2 * kStQ, kStExp = 3 * kStQ, kStW = 4 * kStQ, kStCol = 5 * kStQ,
+              kStTab = 6 * kStQ;
 __host__ __device__ constexpr size_t st_smem_bytes(int n, bool states) {
   return 1024 + (states ? 2 : 3) * size_t(st_tile_bytes(n)) + 2 * st_tile_bytes(kStP) +
-         (states ? 0 : size_t(2) * 2 * kStP * n * 2) + size_t(4) * 4 * kStTab;
+         size_t(2) * 2 * kStP * n * 2 + size_t(4) * 4 * kStTab;
 }
 
 DFSSM_DEV uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t lbo) {
@@ -80,6 +82,8 @@ DFSSM_DEV void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
 }
 DFSSM_DEV void bar_compute() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+DFSSM_DEV void bar_group(int wg) { asm volatile("bar.sync %0, 128;" :: "r"(2 + wg) : "memory"); }
+
 struct StBars {
   uint64_t fullB[2], emptyB[2], tabA[2], tabX[2], tabE[2];
   uint64_t fullC, emptyC, fullX, emptyX, d1, mready, m2done, ydone, wready, sdone, dfree, hready, done;
@@ -105,7 +109,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   unsigned char* const sX = sB + 2 * TB;                             // [2 heads][128 rows][128 B]
   unsigned char* const sC = sX + 2 * TX;
   unsigned char* const sH = sC + (STATES ? 0 : TB);                  // [2 heads][hi, lo][halves][64 rows][128 B]
-  float* const tab = reinterpret_cast<float*>(sH + (STATES ? 0 : 2 * 2 * kStP * N * 2));   // [2][2][kStTab]
+  float* const tab = reinterpret_cast<float*>(sH + 2 * 2 * kStP * N * 2);   // [2][2][kStTab]
 
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -264,16 +268,21 @@ __global__ void __launch_bounds__(kStThreads, 1)
     // ---- step sizes and tables of head h0 + hd: lane = four rows
     const int hd = warp - 10, h = h0 + hd;
     const double rate = chunks ? -exp(double(a.A_log[h])) : 0.0, log2e = 1.4426950408889634;
+    const float bias = a.dt_bias[h];
     double seg = 0.0;
+    float next[4];                  // raw step sizes of the chunk to come
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) next[j] = scan_raw(a, min(w.t0 + c * kStQ + 4 * lane + j, w.t1 - 1), h);
+    };
+    if (chunks > 0) fetch(0);
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, r0 = w.t0 + c * kStQ, n = min(kStQ, w.t1 - r0);
       float dt[4];
       double cs[4], run = 0.0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = 4 * lane + j;
-        dt[j] = t < n ? scan_dt(a, r0 + t, h) : 0.f;
-      }
+      for (int j = 0; j < 4; ++j) dt[j] = 4 * lane + j < n ? softplus_f(next[j] + bias) : 0.f;
+      if (c + 1 < chunks) fetch(c + 1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         run += double(dt[j]) * rate;
@@ -312,6 +321,11 @@ __global__ void __launch_bounds__(kStThreads, 1)
         *reinterpret_cast<float4*>(tb + kStLo + 4 * lane) = make_float4(lo[0], lo[1], lo[2], lo[3]);
         *reinterpret_cast<float4*>(tb + kStDt + 4 * lane) = make_float4(dt[0], dt[1], dt[2], dt[3]);
         *reinterpret_cast<float4*>(tb + kStExp + 4 * lane) = make_float4(ex[0], ex[1], ex[2], ex[3]);
+        const double last = __shfl_sync(0xffffffffu, cs[3], lane | 7);
+        float col[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) col[j] = exp2_f(float((last - cs[j]) * log2e)) * dt[j];
+        *reinterpret_cast<float4*>(tb + kStCol + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
         if (lane == 0) scal[b][hd][1] = dmax;
       }
       if (lane == 0) scal[b][hd][0] = exp2_f(float(total * log2e));
@@ -348,19 +362,41 @@ __global__ void __launch_bounds__(kStThreads, 1)
     const int hy = h0 + wg;                                  // M, y: head, row t = L
     const float Dh = a.D ? a.D[hy] : 0.f;
     float hs[NH];
-    TS* const state = a.state ? static_cast<TS*>(a.state) + ((size_t(slot) * a.H + h0 + hd) * kStP + p) * N + NH * wg : nullptr;
-    float* const seg_state = a.seg_state + ((size_t(blockIdx.x) * a.H + h0 + hd) * kStP + p) * N + NH * wg;
-    {
-      const bool fresh = a.q.fresh && a.q.fresh[w.s];
-#pragma unroll
-      for (int j = 0; j < NH; ++j) hs[j] = 0.f;
-      if (!STATES && w.count > 1) {
-#pragma unroll
-        for (int j = 0; j < NH; j += 4) ldv<4>(seg_state + j, reinterpret_cast<float(&)[4]>(hs[j]));
-      } else if (!STATES && state && !fresh) {
-#pragma unroll
-        for (int j = 0; j < NH; j += 4) ldv<4>(state + j, reinterpret_cast<float(&)[4]>(hs[j]));
+    // the two heads' states, [128][N] in global memory, pass through shared memory (the
+    // place of H) so that whole lines move: piece j of row r at j ^ (r mod 8)
+    const size_t pair_at = (size_t(STATES || w.count > 1 ? blockIdx.x : slot) * a.H + h0) * kStP * N;
+    auto piece = [&](int r, int j) { return reinterpret_cast<float4*>(sH) + r * (N / 4) + (j ^ (r & 7)); };
+    auto load_state = [&](const auto* from) {
+#pragma unroll 4
+      for (int i = tid; i < 2 * kStP * N / 4; i += 256) {
+        float v[4];
+        ldv<4>(from + 4 * i, v);
+        *piece(i / (N / 4), i % (N / 4)) = make_float4(v[0], v[1], v[2], v[3]);
       }
+      bar_compute();
+#pragma unroll
+      for (int j = 0; j < NH / 4; ++j) {
+        const float4 v = *piece(L, NH / 4 * wg + j);
+        hs[4 * j] = v.x; hs[4 * j + 1] = v.y; hs[4 * j + 2] = v.z; hs[4 * j + 3] = v.w;
+      }
+    };
+    auto store_state = [&](auto* to) {
+#pragma unroll
+      for (int j = 0; j < NH / 4; ++j)
+        *piece(L, NH / 4 * wg + j) = make_float4(hs[4 * j], hs[4 * j + 1], hs[4 * j + 2], hs[4 * j + 3]);
+      bar_compute();
+#pragma unroll 4
+      for (int i = tid; i < 2 * kStP * N / 4; i += 256) {
+        const float4 v = *piece(i / (N / 4), i % (N / 4));
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        stv<4>(to + 4 * i, f);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < NH; ++j) hs[j] = 0.f;
+    if (!STATES) {
+      if (w.count > 1) load_state(static_cast<const float*>(a.seg_state) + pair_at);
+      else if (a.state && !(a.q.fresh && a.q.fresh[w.s])) load_state(static_cast<const TS*>(a.state) + pair_at);
     }
     // H into shared memory as fp16 pieces for chunk c
     auto put_h = [&](int c) {
@@ -416,47 +452,62 @@ __global__ void __launch_bounds__(kStThreads, 1)
         const float thi = te[kStHi + L], tlo = te[kStLo + L];
         wait(bars.d1, c);
         tc_fence_after();
-        float m = 0.f;
+        float m = 0.f, v[32];
 #pragma unroll 1
-        for (int s0 = 0; s0 <= 32 * q; s0 += 32) {
-          float v[32];
+        for (int s0 = 0; s0 < 32 * q; s0 += 32) {
           tmem_ld32(tl + s0, v);
           tmem_wait_ld();
-          const int last = L - s0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) m = fmaxf(m, i <= last ? fabsf(v[i]) : 0.f);
+          for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
         }
+        tmem_ld32(tl + 32 * q, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m = fmaxf(m, i <= lane ? fabsf(v[i]) : 0.f);
         const int k = scale_of(m * dmax);
         const float up = pow2_f(k);
         ytop = pow2_f(-k);
+        const uint32_t tm = tl + 128 + 128 * wg;
+        uint32_t hi[16], lo[16];
+        // the 32 columns of the warp's own rows
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 eh = *reinterpret_cast<const float4*>(te + kStHi + 32 * q + i);
+          const float4 el = *reinterpret_cast<const float4*>(te + kStLo + 32 * q + i);
+          const float4 ds = *reinterpret_cast<const float4*>(te + kStDt + 32 * q + i);
+          const float e[4] = {(thi - eh.x) + (tlo - el.x), (thi - eh.y) + (tlo - el.y), (thi - eh.z) + (tlo - el.z),
+                              (thi - eh.w) + (tlo - el.w)};
+          const float d[4] = {ds.x, ds.y, ds.z, ds.w};
+          float r[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[j] = i + j <= lane ? (v[i + j] * up) * (exp2_f(e[j]) * d[j]) : 0.f;
+          split_h2(r[0], r[1], hi[i / 2], lo[i / 2]);
+          split_h2(r[2], r[3], hi[i / 2 + 1], lo[i / 2 + 1]);
+        }
+        tmem_st16(tm + 16 * q, hi);
+        tmem_st16(tm + 64 + 16 * q, lo);
+        // earlier columns: with e the last row of their 32, exp(cs_t - cs_s) is exp(cs_t - cs_e)
+        // exp(cs_e - cs_s), neither above 1: one exponential per row and 32 columns
 #pragma unroll 1
-        for (int s0 = 0; s0 < kStQ; s0 += 32) {
-          uint32_t hi[16], lo[16];
-          if (s0 <= 32 * q) {
-            float v[32];
-            tmem_ld32(tl + s0, v);
-            tmem_wait_ld();
-            const int last = L - s0;
+        for (int s0 = 0; s0 < 32 * q; s0 += 32) {
+          const float f = up * exp2_f((thi - te[kStHi + s0 + 31]) + (tlo - te[kStLo + s0 + 31]));
+          tmem_ld32(tl + s0, v);
+          tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 eh = *reinterpret_cast<const float4*>(te + kStHi + s0 + i);
-              const float4 el = *reinterpret_cast<const float4*>(te + kStLo + s0 + i);
-              const float4 ds = *reinterpret_cast<const float4*>(te + kStDt + s0 + i);
-              const float e[4] = {(thi - eh.x) + (tlo - el.x), (thi - eh.y) + (tlo - el.y), (thi - eh.z) + (tlo - el.z),
-                                  (thi - eh.w) + (tlo - el.w)};
-              const float d[4] = {ds.x, ds.y, ds.z, ds.w};
-              float r[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) r[j] = i + j <= last ? (v[i + j] * up) * (exp2_f(e[j]) * d[j]) : 0.f;
-              split_h2(r[0], r[1], hi[i / 2], lo[i / 2]);
-              split_h2(r[2], r[3], hi[i / 2 + 1], lo[i / 2 + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0u;
+          for (int i = 0; i < 32; i += 4) {
+            const float4 cf = *reinterpret_cast<const float4*>(te + kStCol + s0 + i);
+            split_h2((v[i] * f) * cf.x, (v[i + 1] * f) * cf.y, hi[i / 2], lo[i / 2]);
+            split_h2((v[i + 2] * f) * cf.z, (v[i + 3] * f) * cf.w, hi[i / 2 + 1], lo[i / 2 + 1]);
           }
-          tmem_st16(tl + 128 + 128 * wg + s0 / 2, hi);
-          tmem_st16(tl + 128 + 128 * wg + 64 + s0 / 2, lo);
+          tmem_st16(tm + s0 / 2, hi);
+          tmem_st16(tm + 64 + s0 / 2, lo);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) hi[i] = 0u;
+#pragma unroll 1
+        for (int s0 = 32 * q + 32; s0 < kStQ; s0 += 32) {
+          tmem_st16(tm + s0 / 2, hi);
+          tmem_st16(tm + 64 + s0 / 2, hi);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -493,39 +544,57 @@ __global__ void __launch_bounds__(kStThreads, 1)
         tc_fence_before();
         arrive(bars.wready);
         if (STATES) arrive(bars.emptyX);
+        else bar_compute();            // X has been read: its rows take y's on the way out
       }
       if (!STATES) {
-        // y
-        const float* te = tb + wg * kStTab;
-        const float et = te[kStExp + L];
+        // y: row L of head wg into its row of X, 128 bytes at a time, and from there to global
+        // memory in whole lines
+        constexpr int PC = 128 / int(sizeof(TY)), RD = kStP / PC;      // columns of a piece, pieces
+        const float et = tb[wg * kStTab + kStExp + L];
+        unsigned char* const xrow = sX + wg * TX + L * 128;
+        uint4 xv[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xv[j] = *reinterpret_cast<const uint4*>(xrow + ((j ^ (L & 7)) << 4));
         wait(bars.ydone, c);
         tc_fence_after();
         const float f2 = et * hinv[c & 1][wg];
-        TY* yp = static_cast<TY*>(a.y.p) + (long long)(r0 + L) * a.y.stride + hy * kStP;
-#pragma unroll 1
-        for (int j = 0; j < kStP; j += 16) {
-          float y1[16], y2[16], out[16];
-          tmem_ld16(tl + 384 + 64 * wg + j, y1);
-          tmem_ld16(tl + 64 * wg + j, y2);
-          tmem_wait_ld();
+        TY* const yp = static_cast<TY*>(a.y.p) + (long long)r0 * a.y.stride + hy * kStP;
 #pragma unroll
-          for (int i = 0; i < 16; i += 8) {
-            const uint4 xv = *reinterpret_cast<const uint4*>(sX + wg * TX + L * 128 + ((((j + i) >> 3) ^ (L & 7)) << 4));
-            const uint32_t u[4] = {xv.x, xv.y, xv.z, xv.w};
+        for (int rd = 0; rd < RD; ++rd) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
-              out[i + 2 * k] = fmaf(Dh, f.x, fmaf(y2[i + 2 * k], f2, y1[i + 2 * k] * ytop));
-              out[i + 2 * k + 1] = fmaf(Dh, f.y, fmaf(y2[i + 2 * k + 1], f2, y1[i + 2 * k + 1] * ytop));
+          for (int j = rd * PC; j < (rd + 1) * PC; j += 16) {
+            float y1[16], y2[16], out[16];
+            tmem_ld16(tl + 384 + 64 * wg + j, y1);
+            tmem_ld16(tl + 64 * wg + j, y2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const uint4 u = xv[(j + i) / 8];
+              const uint32_t word = (i & 6) == 0 ? u.x : (i & 6) == 2 ? u.y : (i & 6) == 4 ? u.z : u.w;
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&word));
+              out[i] = fmaf(Dh, f.x, fmaf(y2[i], f2, y1[i] * ytop));
+              out[i + 1] = fmaf(Dh, f.y, fmaf(y2[i + 1], f2, y1[i + 1] * ytop));
+            }
+            constexpr int E = 16 / int(sizeof(TY));
+#pragma unroll
+            for (int i = 0; i < 16; i += E) {
+              const int ch = (j + i) % PC / E;
+              stv<E>(reinterpret_cast<TY*>(xrow + ((ch ^ (L & 7)) << 4)), reinterpret_cast<float(&)[E]>(out[i]));
             }
           }
-          if (L < n) {
-            stv<8>(yp + j, reinterpret_cast<float(&)[8]>(out[0]));
-            stv<8>(yp + j + 8, reinterpret_cast<float(&)[8]>(out[8]));
+          if (rd == RD - 1) {
+            tc_fence_before();
+            arrive(bars.dfree);
           }
+          bar_group(wg);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 16 * i + (tid & 127) / 8, ch = tid & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(sX + wg * TX + r * 128 + ((ch ^ (r & 7)) << 4));
+            if (r < n) *reinterpret_cast<uint4*>(yp + (long long)r * a.y.stride + rd * PC + ch * (16 / int(sizeof(TY)))) = v;
+          }
+          if (rd + 1 < RD) bar_group(wg);
         }
-        tc_fence_before();
-        arrive(bars.dfree);
         arrive(bars.emptyX);
       }
       // H
@@ -544,13 +613,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
       arrive(bars.tabE[b]);
       if (!STATES && c + 1 < chunks) put_h(c + 1);      // its barrier also keeps M's stores behind S's loads
     }
-    if (STATES) {
-#pragma unroll
-      for (int j = 0; j < NH; j += 4) stv<4>(seg_state + j, reinterpret_cast<float(&)[4]>(hs[j]));
-    } else if (state && w.k == w.count - 1) {
-#pragma unroll
-      for (int j = 0; j < NH; j += 4) stv<4>(state + j, reinterpret_cast<float(&)[4]>(hs[j]));
-    }
+    if (STATES) store_state(a.seg_state + pair_at);
+    else if (a.state && w.k == w.count - 1) store_state(static_cast<TS*>(a.state) + (size_t(slot) * a.H + h0) * kStP * N);
   }
   tc_fence_before();
   __syncthreads();
