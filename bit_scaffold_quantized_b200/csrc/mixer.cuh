@@ -93,7 +93,8 @@ DFSSM_DEV void stv(__half* p, const float (&v)[VEC]) {
 // 2^126 gives 0, where the exact value is below 1e-36.
 DFSSM_DEV float silu_f(float v) { return __fdividef(v, 1.f + expf(-v)); }
 
-DFSSM_DEV float softplus_f(float v) { return v > 20.f ? v : log1pf(expf(v)); }
+// log(1 + e^v) without a branch; for v > 20 it is v to fp32's last bit.
+DFSSM_DEV float softplus_f(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 
 // Rows [b, e) of sequence s; false where they break the rule.
 DFSSM_DEV bool seq_rows(const Seqs& q, int s, int& b, int& e) {
