@@ -22,18 +22,6 @@ namespace {
 constexpr size_t kNone = ~size_t(0);
 constexpr int kHeadBlocks = 592;  // 4 per SM on a 148-SM B200
 
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
-
-struct Bump {
-  size_t off = 0;
-  size_t take(size_t bytes) {
-    off = align256(off);
-    size_t at = off;
-    off += bytes;
-    return at;
-  }
-};
-
 size_t tiled_words(int rows, int cols) {
   return size_t((rows + kTileRows - 1) / kTileRows) * kTileRows * (cols / 32);
 }

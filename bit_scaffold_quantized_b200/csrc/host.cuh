@@ -97,6 +97,19 @@ cudaError_t launch_chain(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t
     if (e_ != cudaSuccess) return fail(DFSSM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e_)); \
   } while (0)
 
+// Workspace layout: regions one behind the other at 256-byte boundaries.
+inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct Bump {
+  size_t off = 0;
+  size_t take(size_t bytes) {
+    off = align256(off);
+    size_t at = off;
+    off += bytes;
+    return at;
+  }
+};
+
 inline int current_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {

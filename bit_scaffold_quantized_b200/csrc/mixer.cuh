@@ -332,7 +332,12 @@ struct ScanArgs {
   int seg, max_segs;
   float* seg_state;      // [max_segs][H][P][N]
   float* seg_decay;      // [max_segs][H]: decay over the segment
+  // k_scan_tc: chunks of kStQ rows, numbered as segments of that length would be
+  float* rec;            // [chunks][H][kStRec]: see k_scan_steps
+  float* big;            // [chunks][G][2]: the largest |B| and |C|
 };
+
+constexpr int kStQ = 128;
 
 DFSSM_DEV float scan_raw(const ScanArgs& a, long long row, int h) {
   const long long at = row * a.dt.stride + h;

@@ -148,8 +148,9 @@ bool scan_tc_shape(const dfssm_scan* s, int dtype) {
 // Segments of the prompt form: enough blocks for the SMs, and not much shorter than what
 // the states between segments cost to move.
 struct ScanPlan {
-  int seg, max_segs;
-  size_t decay_at, bytes;
+  int seg, max_segs, max_chunks;
+  bool split;                                      // more than one segment
+  size_t decay_at, rec_at, big_at, bytes;
 };
 
 ScanPlan scan_plan(const dfssm_scan* s, bool tc, int n_seqs, int n_rows) {
@@ -158,16 +159,17 @@ ScanPlan scan_plan(const dfssm_scan* s, bool tc, int n_seqs, int n_rows) {
   const long long want = tc ? 2LL * sm_count() : 4LL * sm_count();
   long long seg = ((long long)n_rows * heads + want - 1) / want;
   seg = std::max<long long>(tc ? 2 * kStQ : 4 * kScanQ, (seg + unit - 1) / unit * unit);
-  if (seg >= n_rows) {
-    p.seg = int(seg);
-    p.max_segs = n_seqs;
-    p.decay_at = p.bytes = 0;
-    return p;
-  }
   p.seg = int(seg);
-  p.max_segs = n_rows / p.seg + n_seqs;
-  p.decay_at = (size_t(4) * p.max_segs * s->nheads * s->headdim * s->d_state + 255) & ~size_t(255);
-  p.bytes = p.decay_at + size_t(4) * p.max_segs * s->nheads;
+  p.split = seg < n_rows;
+  p.max_segs = p.split ? n_rows / p.seg + n_seqs : n_seqs;
+  p.max_chunks = tc ? n_rows / kStQ + n_seqs : 0;
+  Bump bp;
+  const size_t segs = p.split ? p.max_segs : 0, H = s->nheads;
+  bp.take(4 * segs * H * s->headdim * s->d_state);
+  p.decay_at = bp.take(4 * segs * H);
+  p.rec_at = bp.take(size_t(4) * kStRec * p.max_chunks * H);
+  p.big_at = bp.take(size_t(8) * p.max_chunks * s->ngroups);
+  p.bytes = align256(bp.off);
   return p;
 }
 
@@ -246,7 +248,7 @@ int scan_map(CUtensorMap* map, const Rows& r, long long cols, int n_rows) {
 }
 
 template <typename TY, typename TS, int N>
-int scan_tc_launch(const ScanArgs& a, cudaStream_t st) {
+int scan_tc_launch(const ScanArgs& a, int chunks, cudaStream_t st) {
   CUtensorMap mx, mb, mc;
   int rc;
   if ((rc = scan_map(&mx, a.x, (long long)a.H * a.P, a.q.n_rows)) ||
@@ -259,6 +261,7 @@ int scan_tc_launch(const ScanArgs& a, cudaStream_t st) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k_scan_tc<float, TS, N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(states));
   if (e != cudaSuccess) return fail(DFSSM_ERR_CUDA, "k_scan_tc smem attribute: %s", cudaGetErrorString(e));
+  CHAIN_LAUNCH("k_scan_steps", k_scan_steps<N>, dim3(chunks, (a.H + 7) / 8), dim3(256), 0, st, 0, a);
   if (a.seg_state) {
     CHAIN_LAUNCH("k_scan_tc", k_scan_tc<float, TS, N, true>, grid, dim3(kStThreads), states, st, 0, a, mx, mb, mc);
     CHAIN_LAUNCH("k_scan_join", k_scan_join<TS>, dim3(a.q.n_seqs, a.H, (a.P * a.N + 1023) / 1024), dim3(256), 0, st, 0, a);
@@ -462,16 +465,19 @@ int dfssm_scan_prompt(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows
   const ScanPlan p = scan_plan(s, tc, seqs->n_seqs, seqs->n_rows);
   a.seg = p.seg;
   a.max_segs = p.max_segs;
-  if (p.bytes) {
-    a.seg_state = static_cast<float*>(ws);
-    a.seg_decay = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + p.decay_at);
+  auto at = [&](size_t off) { return reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + off); };
+  if (p.split) {
+    a.seg_state = at(0);
+    a.seg_decay = at(p.decay_at);
   }
+  a.rec = at(p.rec_at);
+  a.big = at(p.big_at);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (tc) {
     rc = by_types(s->state_dtype, y->dtype, [&](auto ts, auto ty) {
       using TS = decltype(ts);
       using TY = decltype(ty);
-      return s->d_state == 64 ? scan_tc_launch<TY, TS, 64>(a, st) : scan_tc_launch<TY, TS, 128>(a, st);
+      return s->d_state == 64 ? scan_tc_launch<TY, TS, 64>(a, p.max_chunks, st) : scan_tc_launch<TY, TS, 128>(a, p.max_chunks, st);
     });
     return rc ? rc : ok();
   }

@@ -16,8 +16,9 @@ namespace dfssm {
 //   y_t = Y1 + exp(cs_t) Y2,   H <- exp(cs_Q) H + S;   D x_t comes in as D added to M[t][t].
 // x, B and C are operands as they are (fp16 is exact); M, H and W are fp32 values and go in
 // as two fp16 pieces, value = hi + lo to 2^-22, two products each, scaled by a power of two
-// (per row of M, per head of H and W) so that the largest lies below 2^14: fp16 then holds
-// the pieces of everything down to 2^-28 of it.  (With one piece of M and H the kernel takes
+// per head and chunk that a bound on the largest keeps below 2^14: fp16 then holds the
+// pieces of everything down to 2^-28 of the bound, and the bounds (products of the largest
+// |B|, |C|, |x| and dt) are good to 2^12 or so.  (With one piece of M and H the kernel takes
 // 14 % less time, but the rows of a short prompt come out up to 2.5 half steps of fp16 off.)
 // Accumulation is fp32 in tensor memory, the state fp32 in registers.
 //   warps 0..15  arithmetic, in four warpgroups.  For M and y: thread = row t (TMEM lane),
@@ -30,9 +31,10 @@ namespace dfssm {
 //                as its last reader is done, a good part of a chunk before it is needed;
 //                without C there is room for two X);
 //   warp 17      MMA issuer;
-//   warps 18, 19 a head each, one chunk ahead: step sizes, running sums (fp64) and their
-//                tables.  cs is kept as two floats, hi + lo: near differences are then good to
-//                2^-24 of their own size however far the sum has run (a step may be huge).
+//   warps 18, 19 a head each: the chunk's largest |x|, W's factors, the scales.
+// k_scan_steps goes before: the step sizes, their running sums (fp64) and the tables of
+// every chunk and head.  cs is kept as two floats, hi + lo: near differences are then good to
+// 2^-24 of their own size however far the sum has run (a step may be huge).
 // Tensor memory (columns): CB [0,128), then Y1 of both heads; Y2 of both [128,256); M of head 0
 // [256,384) as hi | lo, then S; M of head 1 [384,512), then W.  CB and Y2 are issued as
 // soon as the chunk's B and C are there, so that only Y1 and S are waited for.
@@ -40,20 +42,23 @@ namespace dfssm {
 // their sequence's last; see k_scan_join.
 // Every wait is bounded; one that gives up sets the status bit, the roles run through
 // their loops without waiting, and the block ends as usual.
-constexpr int kStQ = 128;
 constexpr int kStWarps = 16;                   // of the arithmetic
 constexpr int kStCompute = 32 * kStWarps;
 constexpr int kStThreads = kStCompute + 128;
 constexpr int kStP = 64;
 
 __host__ __device__ constexpr int st_tile_bytes(int n) { return kStQ * n * 2; }
-// Tables of a chunk and head: cs log2 e as hi and lo, dt, exp(cs), W's factors, and
-// exp(cs_e - cs_s) dt_s with e the last row of the 32 that s belongs to.
-constexpr int kStHi = 0, kStLo = kStQ, kStDt = 2 * kStQ, kStExp = 3 * kStQ, kStW = 4 * kStQ, kStCol = 5 * kStQ,
-              kStTab = 6 * kStQ;
+// The record of a chunk and head: cs log2 e as hi and lo, dt, exp(cs_Q - cs_s) dt_s, and
+// exp(cs_e - cs_s) dt_s with e the last row of the 32 that s belongs to; then exp(cs_Q), the
+// largest dt, the largest of the fourth table, cs_Q log2 e.  In shared memory W's factors,
+// scaled, come behind it.
+constexpr int kStHi = 0, kStLo = kStQ, kStDt = 2 * kStQ, kStRaw = 3 * kStQ, kStCol = 4 * kStQ, kStMeta = 5 * kStQ,
+              kStRec = 5 * kStQ + 16, kStW = kStRec, kStTab = kStRec + kStQ;
+// The place of H, which states pass through on their way in and out and y on its way out.
+__host__ __device__ constexpr int st_h_bytes(int n, bool states) { return states ? 2 * kStP * n * 4 : 2 * kStQ * kStP * 4; }
 __host__ __device__ constexpr size_t st_smem_bytes(int n, bool states) {
   return 1024 + (states ? 2 : 3) * size_t(st_tile_bytes(n)) + (states ? 4 : 2) * st_tile_bytes(kStP) +
-         size_t(2) * 2 * kStP * n * 2 + size_t(4) * 4 * kStTab;
+         st_h_bytes(n, states) + size_t(4) * 4 * kStTab;
 }
 
 DFSSM_DEV uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t lbo) {
@@ -96,8 +101,102 @@ DFSSM_DEV void bar_head(int head) {
   else asm volatile("bar.sync 2, %0;" :: "n"(kStCompute / 2) : "memory");
 }
 
+// Step sizes, running sums and tables of every chunk (grid x, numbered as segments are) and
+// head (grid y: eight heads a block, a warp each; lane = four rows), and the largest finite
+// |B| and |C| of the chunk.  With less of this in k_scan_tc (two warps did it there, six
+// thousand cycles a chunk) nothing waits for it.
+template <int N>
+__global__ void __launch_bounds__(256) k_scan_steps(ScanArgs a) {
+  pdl_wait();
+  pdl_release();
+  __shared__ float top[8][2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  SegWork w;
+  a.seg = kStQ;                       // chunks are numbered as segments of one chunk
+  if (!seg_find(a, blockIdx.x, w)) return;
+  const int n = w.t1 - w.t0, h = blockIdx.y * 8 + warp;
+  if (h < a.H) {
+    const double rate = -exp(double(a.A_log[h])), log2e = 1.4426950408889634;
+    const float bias = a.dt_bias[h];
+    float dt[4], dmax = 0.f, big = 0.f, hi[4], lo[4], raw[4], col[4];
+    double cs[4], run = 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dt[j] = scan_raw(a, min(w.t0 + 4 * lane + j, w.t1 - 1), h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      dt[j] = 4 * lane + j < n ? softplus_f(dt[j] + bias) : 0.f;
+      run += double(dt[j]) * rate;
+      cs[j] = run;
+    }
+    double up = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double v = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += v;
+    }
+    const double total = __shfl_sync(0xffffffffu, up, 31);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cs[j] += up - run;
+    const double last = __shfl_sync(0xffffffffu, cs[3], lane | 7);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const double e = cs[j] * log2e;
+      hi[j] = float(e);
+      lo[j] = float(e - double(hi[j]));
+      raw[j] = exp2_f(float((total - cs[j]) * log2e)) * dt[j];
+      col[j] = exp2_f(float((last - cs[j]) * log2e)) * dt[j];
+      dmax = fmaxf(dmax, dt[j]);
+      big = fmaxf(big, raw[j]);
+    }
+    dmax = warp_max(dmax);
+    big = warp_max(big);
+    float* rec = a.rec + (size_t(blockIdx.x) * a.H + h) * kStRec;
+    *reinterpret_cast<float4*>(rec + kStHi + 4 * lane) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<float4*>(rec + kStLo + 4 * lane) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<float4*>(rec + kStDt + 4 * lane) = make_float4(dt[0], dt[1], dt[2], dt[3]);
+    *reinterpret_cast<float4*>(rec + kStRaw + 4 * lane) = make_float4(raw[0], raw[1], raw[2], raw[3]);
+    *reinterpret_cast<float4*>(rec + kStCol + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
+    if (lane == 0)
+      *reinterpret_cast<float4*>(rec + kStMeta) =
+          make_float4(exp2_f(float(total * log2e)), dmax, big, float(total * log2e));
+  }
+  if (blockIdx.y > 0) return;
+  for (int g = 0; g < a.G; ++g) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const Rows& r = which ? a.C : a.B;
+      const __half* p = static_cast<const __half*>(r.p) + g * N;
+      uint32_t m = 0;               // the larger half of each pair, as bits: below 0x7c00 is finite
+#pragma unroll 4
+      for (int i = tid; i < kStQ * (N / 8); i += 256) {
+        const int row = i / (N / 8);
+        if (row < n) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p + (w.t0 + row) * r.stride + 8 * (i % (N / 8)));
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t x = u[k] & 0x7fffu, y = (u[k] >> 16) & 0x7fffu;
+            m = max(m, x < 0x7c00u ? x : 0u);
+            m = max(m, y < 0x7c00u ? y : 0u);
+          }
+        }
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == 0) top[warp][which] = h2f(uint16_t(m));
+    }
+    __syncthreads();
+    if (tid < 2) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, top[i][tid]);
+      a.big[(size_t(blockIdx.x) * a.G + g) * 2 + tid] = m;
+    }
+    __syncthreads();
+  }
+}
+
 struct StBars {
-  uint64_t fullB[2], emptyB[2], tabA[2], tabX[2], tabE[2];
+  uint64_t fullB[2], emptyB[2], fullT[2], tabA[2], tabX[2], tabE[2];
   uint64_t fullX[2], emptyX[2];      // one of each unless STATES
   uint64_t fullC, emptyC, d1, mready, ydone, wready, sdone, dfree, hready, done;
 };
@@ -108,14 +207,17 @@ __global__ void __launch_bounds__(kStThreads, 1)
               const __grid_constant__ CUtensorMap tm_c) {
   constexpr int TB = st_tile_bytes(N), TX = st_tile_bytes(kStP), HALF = st_tile_bytes(64), NH = N / 4;
   constexpr int XB = STATES ? 2 : 1;     // buffers of X
+  static_assert(st_h_bytes(N, STATES) >= 2 * 2 * kStP * N * 2 && kStTab % 4 == 0, "the place of H, bulk copies");
   constexpr int COLS = STATES ? 256 : 512;
   constexpr uint32_t cY = 128, cM = 256, cS = STATES ? 0 : 256, cW = STATES ? 128 : 384;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) StBars bars;
   __shared__ uint32_t tmem_s;
   __shared__ int fail;
-  __shared__ float scal[2][2][4];        // [buffer][head]: exp(cs_Q), max dt, 2^-k of W
-  __shared__ __align__(16) float wmax[2][2][8], hinv[2][2], mtop[2][2][kStQ];
+  // [buffer][head]: the scale of M, its inverse, the inverse of W's, and the scale of the H
+  // that leaves the chunk
+  __shared__ __align__(16) float scal[2][2][4];
+  __shared__ __align__(16) float wmax[2][8], hbig[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -123,7 +225,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   unsigned char* const sX = sB + 2 * TB;                             // [XB][2 heads][128 rows][128 B]
   unsigned char* const sC = sX + XB * 2 * TX;
   unsigned char* const sH = sC + (STATES ? 0 : TB);                  // [2 heads][hi, lo][halves][64 rows][128 B]
-  float* const tab = reinterpret_cast<float*>(sH + 2 * 2 * kStP * N * 2);   // [2][2][kStTab]
+  float* const tab = reinterpret_cast<float*>(sH + st_h_bytes(N, STATES));   // [2][2][kStTab]
 
   if (warp == kStWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -136,6 +238,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.fullB[i], 1);
       mbar_init(&bars.emptyB[i], 1);
+      mbar_init(&bars.fullT[i], 1);
       mbar_init(&bars.tabA[i], 2);
       mbar_init(&bars.tabX[i], 2);
       mbar_init(&bars.tabE[i], kStWarps);
@@ -176,6 +279,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
     work = slot >= 0;
   }
   const int chunks = work ? (w.t1 - w.t0 + kStQ - 1) / kStQ : 0;
+  const int chunk0 = work ? w.b / kStQ + w.s + (w.t0 - w.b) / kStQ : 0;      // number of the first
 
   if (warp == kStWarps) {
     // ---- TMA
@@ -183,7 +287,14 @@ __global__ void __launch_bounds__(kStThreads, 1)
     int issued = 0;
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, r0 = w.t0 + c * kStQ;
-      bool go = c < 2 || wait(bars.emptyB[b], (c >> 1) - 1);
+      bool go = c < 2 || wait(bars.tabE[b], (c >> 1) - 1);
+      if (one && go) {
+        mbar_expect_tx(&bars.fullT[b], 2 * kStRec * 4);
+        for (int i = 0; i < 2; ++i)
+          bulk_g2s(tab + (2 * b + i) * kStTab, a.rec + (size_t(chunk0 + c) * a.H + h0 + i) * kStRec, kStRec * 4,
+                   &bars.fullT[b]);
+      }
+      go = go && (c < 2 || wait(bars.emptyB[b], (c >> 1) - 1));
       if (one && go) {
         mbar_expect_tx(&bars.fullB[b], TB);
         for (int i = 0; i < N / 64; ++i)
@@ -212,7 +323,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
       for (long long s = 0; s < kTcSpinLimit / 16 && !mbar_try_wait(&bar, unsigned(parity) & 1u); ++s) {
       }
     };
-    for (int c = max(0, issued - 2); c < chunks && c < issued + 1; ++c) landed(bars.fullB[c & 1], c >> 1);
+    for (int c = max(0, issued - 2); c < chunks && c < issued + 1; ++c) {
+      landed(bars.fullT[c & 1], c >> 1);
+      landed(bars.fullB[c & 1], c >> 1);
+    }
     for (int c = max(0, issued - XB); c < issued; ++c) landed(bars.fullX[c % XB], c / XB);
     if (!STATES && issued > 0) landed(bars.fullC, issued - 1);
   } else if (warp == kStWarps + 1) {
@@ -277,80 +391,34 @@ __global__ void __launch_bounds__(kStThreads, 1)
       }
     }
   } else if (warp >= kStWarps + 2) {
-    // ---- step sizes and tables of head h0 + hd: lane = four rows
+    // ---- scales of head h0 + hd
     const int hd = warp - kStWarps - 2, h = h0 + hd;
-    const double rate = chunks ? -exp(double(a.A_log[h])) : 0.0, log2e = 1.4426950408889634;
-    const float bias = chunks ? a.dt_bias[h] : 0.f;
-    double seg = 0.0;
-    float next[4];                  // raw step sizes of the chunk to come
-    float wx[2][4], wtop[2];        // W's factors and the largest, before their scale
-    auto fetch = [&](int c) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) next[j] = scan_raw(a, min(w.t0 + c * kStQ + 4 * lane + j, w.t1 - 1), h);
-    };
-    auto steps = [&](int c, float (&wf)[4], float& top) {
-      const int b = c & 1, n = min(kStQ, w.t1 - w.t0 - c * kStQ);
-      float dt[4], dmax = 0.f;
-      double cs[4], run = 0.0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dt[j] = 4 * lane + j < n ? softplus_f(next[j] + bias) : 0.f;
-      if (c + 1 < chunks) fetch(c + 1);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        run += double(dt[j]) * rate;
-        cs[j] = run;
-      }
-      double up = run;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, up, o);
-        if (lane >= o) up += v;
-      }
-      const double total = __shfl_sync(0xffffffffu, up, 31);
-      top = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        cs[j] += up - run;
-        dmax = fmaxf(dmax, dt[j]);
-        wf[j] = exp2_f(float((total - cs[j]) * log2e)) * dt[j];
-        top = fmaxf(top, wf[j]);
-      }
-      dmax = warp_max(dmax);
-      top = warp_max(top);
-      seg += total;
-      if (c >= 2) wait(bars.tabE[b], (c >> 1) - 1);
-      float* tb = tab + (2 * b + hd) * kStTab;
-      if (!STATES) {
-        float hi[4], lo[4], ex[4], col[4];
-        const double last = __shfl_sync(0xffffffffu, cs[3], lane | 7);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const double e = cs[j] * log2e;
-          hi[j] = float(e);
-          lo[j] = float(e - double(hi[j]));
-          ex[j] = exp2_f(hi[j]);
-          col[j] = exp2_f(float((last - cs[j]) * log2e)) * dt[j];
-        }
-        *reinterpret_cast<float4*>(tb + kStHi + 4 * lane) = make_float4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<float4*>(tb + kStLo + 4 * lane) = make_float4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<float4*>(tb + kStDt + 4 * lane) = make_float4(dt[0], dt[1], dt[2], dt[3]);
-        *reinterpret_cast<float4*>(tb + kStExp + 4 * lane) = make_float4(ex[0], ex[1], ex[2], ex[3]);
-        *reinterpret_cast<float4*>(tb + kStCol + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
-        if (lane == 0) scal[b][hd][1] = dmax;
-      }
-      if (lane == 0) scal[b][hd][0] = exp2_f(float(total * log2e));
-      arrive(bars.tabA[b]);
-    };
-    if (chunks > 0) {
-      fetch(0);
-      steps(0, wx[0], wtop[0]);
-    }
+    const float Dh = chunks && a.D ? fabsf(a.D[h]) : 0.f;
+    const float* big = a.big + (size_t(chunk0) * a.G + g) * 2;
+    float bnext = chunks ? big[0] : 0.f, cnext = chunks ? big[1] : 0.f, total = 0.f, hmost = 0.f;
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, n = min(kStQ, w.t1 - w.t0 - c * kStQ);
-      if (c + 1 < chunks) steps(c + 1, wx[1], wtop[1]);
-      // the largest |x| of the chunk bounds W's values
+      float* tb = tab + (2 * b + hd) * kStTab;
+      const float bmax = bnext, cmax = cnext;
+      if (c + 1 < chunks) {
+        bnext = big[(c + 1) * 2 * a.G];
+        cnext = big[(c + 1) * 2 * a.G + 1];
+      }
+      wait(bars.fullT[b], c >> 1);
+      const float4 meta = *reinterpret_cast<const float4*>(tb + kStMeta);
+      total += meta.w;
+      if (!STATES) {
+        // |M| <= sum_n |C| |B| dt (+ D on the diagonal)
+        const int k = scale_of(fmaf(float(N) * bmax * cmax, meta.y, Dh));
+        if (lane == 0) {
+          scal[b][hd][0] = pow2_f(k);
+          scal[b][hd][1] = pow2_f(-k);
+        }
+        arrive(bars.tabA[b]);
+      }
       wait(bars.fullX[c % XB], c / XB);
       const unsigned char* xt = sX + (2 * (c % XB) + hd) * TX;
+      const __half2 most = __floats2half2_rn(65504.f, 65504.f);
       __half2 m[4];                    // chains of their own
 #pragma unroll
       for (int k = 0; k < 4; ++k) m[k] = __floats2half2_rn(0.f, 0.f);
@@ -363,23 +431,30 @@ __global__ void __launch_bounds__(kStThreads, 1)
             const uint4 v = *reinterpret_cast<const uint4*>(xt + r * 128 + ((j ^ (r & 7)) << 4));      // no two of 8 lanes in one bank
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m[k] = __hmax2(m[k], __habs2(*reinterpret_cast<const __half2*>(&u[k])));
+            for (int k = 0; k < 4; ++k)
+              m[k] = __hmax2(m[k], __hmin2(__habs2(*reinterpret_cast<const __half2*>(&u[k])), most));
           }
         }
       }
       const __half2 mm = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
       const float xmax = warp_max(fmaxf(__low2float(mm), __high2float(mm)));
-      const int k = scale_of(xmax * wtop[0]);
-      const float up = pow2_f(k);
-      *reinterpret_cast<float4*>(tab + (2 * b + hd) * kStTab + kStW + 4 * lane) =
-          make_float4(wx[0][0] * up, wx[0][1] * up, wx[0][2] * up, wx[0][3] * up);
-      if (lane == 0) scal[b][hd][2] = pow2_f(-k);
+      const int k = scale_of(xmax * meta.z);
+      const float up = pow2_f(k), down = pow2_f(-k);
+      const float4 f = *reinterpret_cast<const float4*>(tb + kStRaw + 4 * lane);
+      *reinterpret_cast<float4*>(tb + kStW + 4 * lane) = make_float4(f.x * up, f.y * up, f.z * up, f.w * up);
+      if (!STATES) {
+        // |H| after the chunk: what enters, kept, and sum_s |W| |B|
+        if (c == 0) {
+          wait(bars.hready, 0);
+          hmost = hbig[hd];
+        }
+        hmost = fmaf(meta.x, hmost, float(kStQ) * (xmax * meta.z) * bmax);
+        if (lane == 0) scal[b][hd][3] = pow2_f(scale_of(hmost));
+      }
+      if (lane == 0) scal[b][hd][2] = down;
       arrive(bars.tabX[b]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) wx[0][j] = wx[1][j];
-      wtop[0] = wtop[1];
     }
-    if (STATES && work && lane == 0) a.seg_decay[size_t(blockIdx.x) * a.H + h] = exp2_f(float(seg * log2e));
+    if (STATES && work && lane == 0) a.seg_decay[size_t(blockIdx.x) * a.H + h] = exp2_f(total);
   } else if (chunks > 0) {
     // ---- arithmetic
     const int wg = warp >> 2, q = warp & 3, L = 32 * q + lane;
@@ -424,20 +499,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
       if (w.count > 1) load_state(static_cast<const float*>(a.seg_state) + pair_at);
       else if (a.state && !(a.q.fresh && a.q.fresh[w.s])) load_state(static_cast<const TS*>(a.state) + pair_at);
     }
-    // H into shared memory as fp16 pieces for chunk c
-    auto put_h = [&](int c) {
-      float m4[4] = {0.f, 0.f, 0.f, 0.f}, m;
-#pragma unroll
-      for (int j = 0; j < NH; ++j) m4[j & 3] = fmaxf(m4[j & 3], fabsf(hs[j]));
-      m = warp_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-      if (lane == 0) wmax[c & 1][hd][2 * wg + (q & 1)] = m;
-      bar_compute();
-      const float4 m0 = *reinterpret_cast<const float4*>(&wmax[c & 1][hd][0]);
-      const float4 m1 = *reinterpret_cast<const float4*>(&wmax[c & 1][hd][4]);
-      m = fmaxf(fmaxf(fmaxf(m0.x, m0.y), fmaxf(m0.z, m0.w)), fmaxf(fmaxf(m1.x, m1.y), fmaxf(m1.z, m1.w)));
-      const int k = scale_of(m);
-      const float up = pow2_f(k);
-      if (p == 0 && wg == 0) hinv[c & 1][hd] = pow2_f(-k);
+    // H into shared memory as fp16 pieces, scaled by up
+    auto put_h = [&](float up) {
 #pragma unroll
       for (int j = 0; j < NH; j += 8) {
         uint32_t hi[4], lo[4];
@@ -451,12 +514,28 @@ __global__ void __launch_bounds__(kStThreads, 1)
       fence_async_smem();
       arrive(bars.hready);
     };
-    if (!STATES) put_h(0);
+    float hdown = 1.f;                    // the inverse of the scale of head hy's H in use
+    if (!STATES) {
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < NH; ++j) m = fmaxf(m, fabsf(hs[j]));
+      m = warp_max(m);
+      if (lane == 0) wmax[hd][2 * wg + (q & 1)] = m;
+      bar_compute();
+      float top[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 m0 = *reinterpret_cast<const float4*>(&wmax[i][0]), m1 = *reinterpret_cast<const float4*>(&wmax[i][4]);
+        top[i] = fmaxf(fmaxf(fmaxf(m0.x, m0.y), fmaxf(m0.z, m0.w)), fmaxf(fmaxf(m1.x, m1.y), fmaxf(m1.z, m1.w)));
+        if (tid == 0) hbig[i] = top[i];
+      }
+      hdown = pow2_f(-scale_of(hy ? top[1] : top[0]));
+      put_h(pow2_f(scale_of(hd ? top[1] : top[0])));
+    }
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, xb = c % XB, r0 = w.t0 + c * kStQ, n = min(kStQ, w.t1 - r0);
       const float* tb = tab + 2 * b * kStTab;
       unsigned char* const xt = sX + 2 * xb * TX;
-      float ytop = 1.f;                                       // 2^-k of this row of M
       if (n < kStQ) {
         // rows behind the sequence's end are another's: zero, as 0 times NaN is no 0
         wait(bars.fullX[xb], c / XB);
@@ -474,33 +553,15 @@ __global__ void __launch_bounds__(kStThreads, 1)
       }
       if (!STATES) {
         // M
-        wait(bars.tabA[b], c >> 1);
         const float* te = tb + hy * kStTab;
-        const float dmax = scal[b][hy][1];
+        wait(bars.fullT[b], c >> 1);
         const float thi = te[kStHi + L], tlo = te[kStLo + L];
+        wait(bars.tabA[b], c >> 1);
+        const float up = scal[b][hy][0];
+        const uint32_t tm = tl + cM + 128 * hy;
         wait(bars.d1, c);
         tc_fence_after();
-        float m4[4] = {0.f, 0.f, 0.f, 0.f}, v[32];
-#pragma unroll 1
-        for (int s0 = 32 * part; s0 <= 32 * q; s0 += 64) {
-          tmem_ld32(tl + s0, v);
-          tmem_wait_ld();
-          if (s0 < 32 * q) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], fabsf(v[i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], i <= lane ? fabsf(v[i]) : 0.f);
-          }
-        }
-        float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        mtop[hy][part][L] = m;
-        bar_head(hy);
-        m = fmaxf(m, mtop[hy][part ^ 1][L]);
-        const int k = scale_of(fmaf(m, dmax, fabsf(Dh)));
-        const float up = pow2_f(k);
-        ytop = pow2_f(-k);
-        const uint32_t tm = tl + cM + 128 * hy;
+        float v[32];
         // With e the last row of the 32 that s belongs to, exp(cs_t - cs_s) = exp(cs_t - cs_e)
         // exp(cs_e - cs_s): one exponential per row and 32 columns.  The second factor is never
         // above 1; the first only in the row's own 32, where it stays below 2^40 unless the
@@ -558,8 +619,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
       }
       // W: rows s = 32 wg .. + 31 of column p of head hd
       {
-        wait(bars.fullX[xb], c / XB);
         wait(bars.tabX[b], c >> 1);
+        wait(bars.fullX[xb], c / XB);
         const float* tw = tb + hd * kStTab + kStW + 32 * wg;
         const unsigned char* xc = xt + hd * TX + 32 * wg * 128 + (p & 7) * 2;
         const int ch = p >> 3;
@@ -583,51 +644,43 @@ __global__ void __launch_bounds__(kStThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         arrive(bars.wready);
-        if (STATES) arrive(bars.emptyX[xb]);
-        else bar_compute();            // X has been read: its rows take y's on the way out
+        arrive(bars.emptyX[xb]);
       }
       if (!STATES) {
-        // y: columns 32 part .. of row L of head hy into the row of X, and from there to global
-        // memory in whole lines; fp32 rows are twice as long and go in two rounds
-        constexpr int E = 16 / int(sizeof(TY)), RD = int(sizeof(TY)) / 2;
-        const float et = tb[hy * kStTab + kStExp + L];
-        unsigned char* const xrow = xt + hy * TX + L * 128;
-        float out[32];
-        const float f2 = et * hinv[c & 1][hy];
+        // y: columns 32 part .. of row L of head hy, to the place of H (whose products are done),
+        // and from there to global memory in whole lines
+        constexpr int E = 16 / int(sizeof(TY)), ROW = kStP * int(sizeof(TY));
+        unsigned char* const yt = sH + hy * kStQ * ROW;
+        const float f1 = scal[b][hy][1], f2 = exp2_f(tb[hy * kStTab + kStHi + L]) * hdown;
 #pragma unroll
         for (int j = 0; j < 32; j += 16) {
-          float y1[16], y2[16];
+          float y1[16], y2[16], out[16];
           tmem_ld16(tl + 64 * hy + 32 * part + j, y1);
           tmem_ld16(tl + cY + 64 * hy + 32 * part + j, y2);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) out[j + i] = fmaf(y2[i], f2, y1[i] * ytop);
+          for (int i = 0; i < 16; ++i) out[i] = fmaf(y2[i], f2, y1[i] * f1);
+#pragma unroll
+          for (int i = 0; i < 16; i += E) {
+            const int ch = (32 * part + j + i) / E;
+            stv<E>(reinterpret_cast<TY*>(yt + L * ROW + ((ch ^ (L & 7)) << 4)), reinterpret_cast<float(&)[E]>(out[i]));
+          }
         }
         tc_fence_before();
         arrive(bars.dfree);
+        hdown = 1.f / scal[b][hy][3];                         // a power of two
+        bar_head(hy);
         TY* const yp = static_cast<TY*>(a.y.p) + (long long)r0 * a.y.stride + (h0 + hy) * kStP;
+        constexpr int CH = ROW / 16;
 #pragma unroll
-        for (int rd = 0; rd < RD; ++rd) {
-          if (RD == 1 || part == rd) {
-#pragma unroll
-            for (int i = 0; i < 32; i += E) {
-              const int ch = (RD == 1 ? 4 * part : 0) + i / E;
-              stv<E>(reinterpret_cast<TY*>(xrow + ((ch ^ (L & 7)) << 4)), reinterpret_cast<float(&)[E]>(out[i]));
-            }
-          }
-          bar_head(hy);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = tid & 255, r = 32 * i + t / 8, ch = t & 7;
-            const uint4 u = *reinterpret_cast<const uint4*>(xt + hy * TX + r * 128 + ((ch ^ (r & 7)) << 4));
-            if (r < n) *reinterpret_cast<uint4*>(yp + (long long)r * a.y.stride + (8 * rd + ch) * E) = u;
-          }
-          if (rd + 1 < RD) bar_head(hy);
+        for (int i = tid & 255; i < kStQ * CH; i += 256) {
+          const int r = i / CH, ch = i % CH;
+          const uint4 u = *reinterpret_cast<const uint4*>(yt + r * ROW + ((ch ^ (r & 7)) << 4));
+          if (r < n) *reinterpret_cast<uint4*>(yp + (long long)r * a.y.stride + ch * E) = u;
         }
-        arrive(bars.emptyX[0]);
       }
       // H
-      const float keep = scal[b][hd][0], down = scal[b][hd][2];
+      const float keep = tb[hd * kStTab + kStMeta], down = scal[b][hd][2], hup = STATES ? 0.f : scal[b][hd][3];
       wait(bars.sdone, c);
       tc_fence_after();
 #pragma unroll
@@ -640,8 +693,12 @@ __global__ void __launch_bounds__(kStThreads, 1)
       }
       tc_fence_before();
       arrive(bars.tabE[b]);
-      if (!STATES && c + 1 < chunks) put_h(c + 1);      // its barrier also keeps M's stores behind S's loads
+      if (!STATES && c + 1 < chunks) {
+        bar_compute();          // y has left H's place; S has been read, M may take its place
+        put_h(hup);
+      }
     }
+    if (!STATES) bar_compute();         // y has left the place
     if (STATES) store_state(a.seg_state + pair_at);
     else if (a.state && w.k == w.count - 1) store_state(static_cast<TS*>(a.state) + (size_t(slot) * a.H + h0) * kStP * N);
   }
