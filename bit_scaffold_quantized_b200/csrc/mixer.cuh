@@ -616,39 +616,39 @@ template <typename TS>
 __global__ void __launch_bounds__(256) k_scan_join(ScanArgs a) {
   pdl_wait();
   pdl_release();
-  const int s = blockIdx.x, h = blockIdx.y, i = 4 * (blockIdx.z * 256 + threadIdx.x);
-  int b, e;
+  const int s = blockIdx.x, h = blockIdx.y;
+  int b, e, slot = -1;
   if (!seq_rows(a.q, s, b, e)) return;
   const int count = (e - b + a.seg - 1) / a.seg;
   if (count <= 1) return;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
   if (a.state) {
-    const int slot = seq_slot(a.q, s, threadIdx.x, 256, [](bool t) { return __syncthreads_or(t) != 0; });
+    slot = seq_slot(a.q, s, threadIdx.x, 256, [](bool t) { return __syncthreads_or(t) != 0; });
     if (slot < 0) return;
-    if (i < a.P * a.N && !(a.q.fresh && a.q.fresh[s]))
-      ldv<4>(static_cast<const TS*>(a.state) + (size_t(slot) * a.H + h) * a.P * a.N + i, v);
   }
-  if (i >= a.P * a.N) return;
-  const int first = seg_first(a, s, b);
-  const size_t step = size_t(a.H) * a.P * a.N;
-  float* at = a.seg_state + (size_t(first) * a.H + h) * a.P * a.N + i;
-  const float* dec = a.seg_decay + size_t(first) * a.H + h;
-  for (int k = 0; k < count; k += kJoinAhead) {       // several segments' loads at a time
-    float own[kJoinAhead][4], d[kJoinAhead];
+  const bool old = slot >= 0 && !(a.q.fresh && a.q.fresh[s]);
+  const size_t size = size_t(a.P) * a.N, step = size * a.H;
+  const float* dec = a.seg_decay + size_t(seg_first(a, s, b)) * a.H + h;
+  for (int i = 4 * (blockIdx.z * 256 + threadIdx.x); i < int(size); i += 1024 * gridDim.z) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (old) ldv<4>(static_cast<const TS*>(a.state) + (size_t(slot) * a.H + h) * size + i, v);
+    float* at = a.seg_state + (size_t(seg_first(a, s, b)) * a.H + h) * size + i;
+    for (int k = 0; k < count; k += kJoinAhead) {       // several segments' loads at a time
+      float own[kJoinAhead][4], d[kJoinAhead];
 #pragma unroll
-    for (int u = 0; u < kJoinAhead; ++u)
-      if (k + u + 1 < count) {
-        ldv<4>(at + (k + u) * step, own[u]);
-        d[u] = dec[size_t(k + u) * a.H];
-      }
+      for (int u = 0; u < kJoinAhead; ++u)
+        if (k + u + 1 < count) {
+          ldv<4>(at + (k + u) * step, own[u]);
+          d[u] = dec[size_t(k + u) * a.H];
+        }
 #pragma unroll
-    for (int u = 0; u < kJoinAhead; ++u)
-      if (k + u < count) {
-        stv<4>(at + (k + u) * step, v);
-        if (k + u + 1 < count)
+      for (int u = 0; u < kJoinAhead; ++u)
+        if (k + u < count) {
+          stv<4>(at + (k + u) * step, v);
+          if (k + u + 1 < count)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], d[u], own[u][j]);
-      }
+            for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], d[u], own[u][j]);
+        }
+    }
   }
 }
 

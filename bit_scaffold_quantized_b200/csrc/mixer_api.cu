@@ -218,6 +218,13 @@ int scan_token_launch(const ScanArgs& a, cudaStream_t st) {
   return go(std::integral_constant<int, 8>{});
 }
 
+// Blocks that share a head's state in k_scan_join: as many as there are values for while
+// (sequence, head) pairs are few.
+int join_blocks(const ScanArgs& a) {
+  const long long pairs = (long long)a.q.n_seqs * a.H, most = (a.P * a.N + 1023) / 1024;
+  return int(std::max(1LL, std::min(most, 8LL * sm_count() / pairs)));
+}
+
 template <typename TX, typename TY, typename TS>
 int scan_prompt_launch(const ScanArgs& a, cudaStream_t st) {
   const size_t smem = scan_smem_bytes(a.P, a.N);
@@ -230,7 +237,7 @@ int scan_prompt_launch(const ScanArgs& a, cudaStream_t st) {
   const dim3 grid(a.max_segs, a.H);
   if (a.seg_state) {
     CHAIN_LAUNCH("k_scan_prompt", k_scan_prompt<TX, TY, TS, true>, grid, dim3(kScanThreads), smem, st, 0, a);
-    CHAIN_LAUNCH("k_scan_join", k_scan_join<TS>, dim3(a.q.n_seqs, a.H, (a.P * a.N + 1023) / 1024), dim3(256), 0, st, 0, a);
+    CHAIN_LAUNCH("k_scan_join", k_scan_join<TS>, dim3(a.q.n_seqs, a.H, join_blocks(a)), dim3(256), 0, st, 0, a);
   }
   CHAIN_LAUNCH("k_scan_prompt", k_scan_prompt<TX, TY, TS, false>, grid, dim3(kScanThreads), smem, st, 0, a);
   return DFSSM_OK;
@@ -261,10 +268,10 @@ int scan_tc_launch(const ScanArgs& a, int chunks, cudaStream_t st) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k_scan_tc<float, TS, N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(states));
   if (e != cudaSuccess) return fail(DFSSM_ERR_CUDA, "k_scan_tc smem attribute: %s", cudaGetErrorString(e));
-  CHAIN_LAUNCH("k_scan_steps", k_scan_steps<N>, dim3(chunks, (a.H + 7) / 8), dim3(256), 0, st, 0, a);
+  CHAIN_LAUNCH("k_scan_steps", k_scan_steps<N>, dim3(chunks, (a.H + 7) / 8 + a.G), dim3(256), 0, st, 0, a);
   if (a.seg_state) {
     CHAIN_LAUNCH("k_scan_tc", k_scan_tc<float, TS, N, true>, grid, dim3(kStThreads), states, st, 0, a, mx, mb, mc);
-    CHAIN_LAUNCH("k_scan_join", k_scan_join<TS>, dim3(a.q.n_seqs, a.H, (a.P * a.N + 1023) / 1024), dim3(256), 0, st, 0, a);
+    CHAIN_LAUNCH("k_scan_join", k_scan_join<TS>, dim3(a.q.n_seqs, a.H, join_blocks(a)), dim3(256), 0, st, 0, a);
   }
   CHAIN_LAUNCH("k_scan_tc", k_scan_tc<TY, TS, N, false>, grid, dim3(kStThreads), smem, st, 0, a, mx, mb, mc);
   return DFSSM_OK;

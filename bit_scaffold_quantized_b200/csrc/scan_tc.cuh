@@ -38,7 +38,8 @@ namespace dfssm {
 // Tensor memory (columns): CB [0,128), then Y1 of both heads; Y2 of both [128,256); M of head 0
 // [256,384) as hi | lo, then S; M of head 1 [384,512), then W.  CB and Y2 are issued as
 // soon as the chunk's B and C are there, so that only Y1 and S are waited for.
-// STATES: only what a segment adds to a zero state (W and S), for segments that are not
+// STATES (W and S twice each, so that a chunk's S is taken up while the next one's W is
+// made): only what a segment adds to a zero state (W and S), for segments that are not
 // their sequence's last; see k_scan_join.
 // Every wait is bounded; one that gives up sets the status bit, the roles run through
 // their loops without waiting, and the block ends as usual.
@@ -102,8 +103,8 @@ DFSSM_DEV void bar_head(int head) {
 }
 
 // Step sizes, running sums and tables of every chunk (grid x, numbered as segments are) and
-// head (grid y: eight heads a block, a warp each; lane = four rows), and the largest finite
-// |B| and |C| of the chunk.  With less of this in k_scan_tc (two warps did it there, six
+// head (grid y: eight heads a block, a warp each; lane = four rows), and (the last G of grid
+// y, a block for each group) the largest finite |B| and |C| of the chunk.  With less of this in k_scan_tc (two warps did it there, six
 // thousand cycles a chunk) nothing waits for it.
 template <int N>
 __global__ void __launch_bounds__(256) k_scan_steps(ScanArgs a) {
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(256) k_scan_steps(ScanArgs a) {
   SegWork w;
   a.seg = kStQ;                       // chunks are numbered as segments of one chunk
   if (!seg_find(a, blockIdx.x, w)) return;
-  const int n = w.t1 - w.t0, h = blockIdx.y * 8 + warp;
+  const int n = w.t1 - w.t0, h = blockIdx.y * 8 + warp, g = int(blockIdx.y) - (a.H + 7) / 8;
   if (h < a.H) {
     const double rate = -exp(double(a.A_log[h])), log2e = 1.4426950408889634;
     const float bias = a.dt_bias[h];
@@ -160,45 +161,43 @@ __global__ void __launch_bounds__(256) k_scan_steps(ScanArgs a) {
       *reinterpret_cast<float4*>(rec + kStMeta) =
           make_float4(exp2_f(float(total * log2e)), dmax, big, float(total * log2e));
   }
-  if (blockIdx.y > 0) return;
-  for (int g = 0; g < a.G; ++g) {
+  if (g < 0) return;
+  uint32_t most[2] = {0u, 0u};      // the larger half of each pair, as bits: below 0x7c00 is finite
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const Rows& r = which ? a.C : a.B;
-      const __half* p = static_cast<const __half*>(r.p) + g * N;
-      uint32_t m = 0;               // the larger half of each pair, as bits: below 0x7c00 is finite
-#pragma unroll 4
-      for (int i = tid; i < kStQ * (N / 8); i += 256) {
-        const int row = i / (N / 8);
-        if (row < n) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p + (w.t0 + row) * r.stride + 8 * (i % (N / 8)));
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  for (int which = 0; which < 2; ++which) {
+    const Rows& r = which ? a.C : a.B;
+    const __half* p = static_cast<const __half*>(r.p) + g * N;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t x = u[k] & 0x7fffu, y = (u[k] >> 16) & 0x7fffu;
-            m = max(m, x < 0x7c00u ? x : 0u);
-            m = max(m, y < 0x7c00u ? y : 0u);
-          }
-        }
+    for (int i = 0; i < kStQ * (N / 8) / 256; ++i) {
+      const int row = (tid + 256 * i) / (N / 8), col = 8 * (tid % (N / 8));
+      const uint4 v = *reinterpret_cast<const uint4*>(p + (w.t0 + min(row, n - 1)) * r.stride + col);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t x = u[k] & 0x7fffu, y = (u[k] >> 16) & 0x7fffu;
+        most[which] = max(most[which], max(x < 0x7c00u ? x : 0u, y < 0x7c00u ? y : 0u));
       }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) top[warp][which] = h2f(uint16_t(m));
     }
-    __syncthreads();
-    if (tid < 2) {
-      float m = 0.f;
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, top[i][tid]);
-      a.big[(size_t(blockIdx.x) * a.G + g) * 2 + tid] = m;
-    }
-    __syncthreads();
+  for (int which = 0; which < 2; ++which) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, most[which]);
+    if (lane == 0) top[warp][which] = h2f(uint16_t(m));
+  }
+  __syncthreads();
+  if (tid < 2) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, top[i][tid]);
+    a.big[(size_t(blockIdx.x) * a.G + g) * 2 + tid] = m;
   }
 }
 
 struct StBars {
   uint64_t fullB[2], emptyB[2], fullT[2], tabA[2], tabX[2], tabE[2];
   uint64_t fullX[2], emptyX[2];      // one of each unless STATES
-  uint64_t fullC, emptyC, d1, mready, ydone, wready, sdone, dfree, hready, done;
+  uint64_t wready[2], sdone[2];            // one of each unless STATES
+  uint64_t fullC, emptyC, d1, mready, ydone, dfree, hready, done;
 };
 
 template <typename TY, typename TS, int N, bool STATES>
@@ -208,8 +207,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
   constexpr int TB = st_tile_bytes(N), TX = st_tile_bytes(kStP), HALF = st_tile_bytes(64), NH = N / 4;
   constexpr int XB = STATES ? 2 : 1;     // buffers of X
   static_assert(st_h_bytes(N, STATES) >= 2 * 2 * kStP * N * 2 && kStTab % 4 == 0, "the place of H, bulk copies");
-  constexpr int COLS = STATES ? 256 : 512;
-  constexpr uint32_t cY = 128, cM = 256, cS = STATES ? 0 : 256, cW = STATES ? 128 : 384;
+  constexpr int COLS = 512;
+  constexpr uint32_t cY = 128, cM = 256, cS = STATES ? 0 : 256, cW = STATES ? 256 : 384;   // STATES: two of each
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) StBars bars;
   __shared__ uint32_t tmem_s;
@@ -242,6 +241,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
       mbar_init(&bars.tabA[i], 2);
       mbar_init(&bars.tabX[i], 2);
       mbar_init(&bars.tabE[i], kStWarps);
+      mbar_init(&bars.wready[i], kStWarps);
+      mbar_init(&bars.sdone[i], 1);
       mbar_init(&bars.fullX[i], 1);
       mbar_init(&bars.emptyX[i], kStWarps);
     }
@@ -250,8 +251,6 @@ __global__ void __launch_bounds__(kStThreads, 1)
     mbar_init(&bars.d1, 1);
     mbar_init(&bars.mready, kStWarps);
     mbar_init(&bars.ydone, 1);
-    mbar_init(&bars.wready, kStWarps);
-    mbar_init(&bars.sdone, 1);
     mbar_init(&bars.dfree, kStWarps);
     mbar_init(&bars.hready, kStWarps);
     mbar_init(&bars.done, 1);
@@ -375,14 +374,16 @@ __global__ void __launch_bounds__(kStThreads, 1)
           tc_commit(&bars.ydone);
         }
       }
-      go = wait(bars.wready, c) && go;
+      const int xb = c % XB;
+      go = wait(bars.wready[xb], c / XB) && go;
       go = __all_sync(0xffffffffu, go);
       tc_fence_after();
       if (one && go) {
         for (int k = 0; k < 2 * kStQ / 16; ++k)
-          umma_f16_ts(tmem + cS, tmem + cW + 8 * k, umma_desc_sw128_mn(aB + b * TB + (k & 7) * 2048, HALF), i4, k > 0);
+          umma_f16_ts(tmem + cS + 128 * xb, tmem + cW + 128 * xb + 8 * k,
+                      umma_desc_sw128_mn(aB + b * TB + (k & 7) * 2048, HALF), i4, k > 0);
         tc_commit(&bars.emptyB[b]);
-        tc_commit(&bars.sdone);
+        tc_commit(&bars.sdone[xb]);
       }
     }
     if (!go) {        // no MMA may still run when the tensor memory is given back
@@ -532,6 +533,23 @@ __global__ void __launch_bounds__(kStThreads, 1)
       hdown = pow2_f(-scale_of(hy ? top[1] : top[0]));
       put_h(pow2_f(scale_of(hd ? top[1] : top[0])));
     }
+    auto take_s = [&](int c, float keep, float down) {
+      wait(bars.sdone[c % XB], c / XB);
+      tc_fence_after();
+#pragma unroll
+      for (int j = 0; j < NH; j += 16) {
+        float v[16];
+        tmem_ld16(tl + cS + 128 * (c % XB) + NH * wg + j, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          hs[j + i] = fmaf(hs[j + i], keep, v[i] * down);
+          hs[j + i + 1] = fmaf(hs[j + i + 1], keep, v[i + 1] * down);
+        }
+      }
+      tc_fence_before();
+    };
+    float keep = 1.f, down = 1.f;         // STATES: of the chunk whose S is on its way
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, xb = c % XB, r0 = w.t0 + c * kStQ, n = min(kStQ, w.t1 - r0);
       const float* tb = tab + 2 * b * kStTab;
@@ -639,11 +657,11 @@ __global__ void __launch_bounds__(kStThreads, 1)
           wait(bars.ydone, c);               // M of head 1 has been read
           tc_fence_after();
         }
-        tmem_st16(tl + cW + 16 * wg, hi);
-        tmem_st16(tl + cW + 64 + 16 * wg, lo);
+        tmem_st16(tl + cW + 128 * xb + 16 * wg, hi);
+        tmem_st16(tl + cW + 128 * xb + 64 + 16 * wg, lo);
         tmem_wait_st();
         tc_fence_before();
-        arrive(bars.wready);
+        arrive(bars.wready[xb]);
         arrive(bars.emptyX[xb]);
       }
       if (!STATES) {
@@ -680,24 +698,22 @@ __global__ void __launch_bounds__(kStThreads, 1)
         }
       }
       // H
-      const float keep = tb[hd * kStTab + kStMeta], down = scal[b][hd][2], hup = STATES ? 0.f : scal[b][hd][3];
-      wait(bars.sdone, c);
-      tc_fence_after();
-#pragma unroll
-      for (int j = 0; j < NH; j += 16) {
-        float v[16];
-        tmem_ld16(tl + cS + NH * wg + j, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) hs[j + i] = fmaf(hs[j + i], keep, v[i] * down);
-      }
-      tc_fence_before();
-      arrive(bars.tabE[b]);
-      if (!STATES && c + 1 < chunks) {
-        bar_compute();          // y has left H's place; S has been read, M may take its place
-        put_h(hup);
+      if (STATES) {
+        if (c > 0) take_s(c - 1, keep, down);
+        keep = tb[hd * kStTab + kStMeta];
+        down = scal[b][hd][2];
+        arrive(bars.tabE[b]);
+      } else {
+        const float hup = scal[b][hd][3];
+        take_s(c, tb[hd * kStTab + kStMeta], scal[b][hd][2]);
+        arrive(bars.tabE[b]);
+        if (c + 1 < chunks) {
+          bar_compute();          // y has left H's place; S has been read, M may take its place
+          put_h(hup);
+        }
       }
     }
+    if (STATES) take_s(chunks - 1, keep, down);
     if (!STATES) bar_compute();         // y has left the place
     if (STATES) store_state(a.seg_state + pair_at);
     else if (a.state && w.k == w.count - 1) store_state(static_cast<TS*>(a.state) + (size_t(slot) * a.H + h0) * kStP * N);
