@@ -89,9 +89,17 @@ DFSSM_DEV void stv(__half* p, const float (&v)[VEC]) {
   }
 }
 
-// v / (1 + e^-v) in fp32: expf and one approximate divide (2 ulp).  A denominator past
-// 2^126 gives 0, where the exact value is below 1e-36.
-DFSSM_DEV float silu_f(float v) { return __fdividef(v, 1.f + expf(-v)); }
+// 2^v, 2 ulp, flushing subnormal results.
+DFSSM_DEV float exp2_f(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// v / (1 + e^-v) in five instructions: the rounding of v log2 e and the two approximate
+// steps leave it within (|v| + 4) 2^-24 of itself.  With expf and its range reduction the conv
+// and the norm were bound by instructions, not memory.
+DFSSM_DEV float silu_f(float v) { return __fdividef(v, 1.f + exp2_f(v * -1.442695041f)); }
 
 // log(1 + e^v) without a branch; for v > 20 it is v to fp32's last bit.
 DFSSM_DEV float softplus_f(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
@@ -108,15 +116,31 @@ DFSSM_DEV bool seq_rows(const Seqs& q, int s, int& b, int& e) {
   return b >= 0 && b <= e && e <= q.n_rows;
 }
 
-// The sequence whose rows hold row t if any does: the last s with start[s] <= t, or -1.
-DFSSM_DEV int seq_find(const Seqs& q, int t) {
-  int lo = 0, hi = q.n_seqs + 1;            // first index with start > t
+constexpr int kSeqScan = 2048;      // sequences up to which a warp counts instead of bisecting
+
+// First index in [0, count) where `past` is true (false, then true, along a valid call's
+// starts; count if nowhere), by a converged warp.  Up to kSeqScan entries every lane looks at
+// its share at once: one round trip to memory where bisecting takes log2(count) of them.
+template <typename Past>
+DFSSM_DEV int warp_first(int count, Past past) {
+  if (count <= kSeqScan) {
+    int below = 0;
+    for (int i = threadIdx.x & 31; i < count; i += 32) below += past(i) ? 0 : 1;
+    return __reduce_add_sync(0xffffffffu, below);
+  }
+  int lo = 0, hi = count;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (q.start[mid] <= t) lo = mid + 1;
-    else hi = mid;
+    if (past(mid)) hi = mid;
+    else lo = mid + 1;
   }
-  return min(lo - 1, q.n_seqs - 1);
+  return lo;
+}
+
+// The sequence whose rows hold row t if any does: the last s with start[s] <= t, or -1.
+// (By a converged warp, t the same for all.)
+DFSSM_DEV int seq_find(const Seqs& q, int t) {
+  return min(warp_first(q.n_seqs + 1, [&](int i) { return q.start[i] > t; }) - 1, q.n_seqs - 1);
 }
 
 // Slot of sequence s, or -1 where it is left out.  `lane` of `lanes` threads share the
@@ -323,6 +347,7 @@ struct ScanArgs {
   Seqs q;
   Rows x, dt, B, C, y;
   int H, P, N, G, dt16;
+  int vec;               // rows of B and C can be read four values at a time
   const float* dt_bias;
   const float* A_log;
   const float* D;
@@ -348,44 +373,54 @@ DFSSM_DEV float scan_dt(const ScanArgs& a, long long row, int h) { return softpl
 constexpr int kTokThreads = 128;
 
 // One token: block = (sequence, head, PASSES * 16 rows of the head's state).  Eight lanes
-// share a state row, four consecutive values each, NJ times; a warp has four rows.
-template <typename TX, typename TY, typename TS, int NJ, int PASSES>
+// share a state row, V consecutive values (16 bytes; 8 for fp16 rows that are no multiple of
+// 16) each, NJ times; a warp has four rows.
+// Nothing but the state's own bytes counts: all of a thread's are asked for at once, before
+// the look at the earlier sequences' slots.
+template <typename TX, typename TY, typename TS, int V, int NJ, int PASSES>
 __global__ void __launch_bounds__(kTokThreads) k_scan_token(ScanArgs a) {
   pdl_wait();
   pdl_release();
   const int s = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int p0 = blockIdx.z * (16 * PASSES) + warp * 4 + (lane >> 3), n0 = 4 * (lane & 7);
+  const int p0 = blockIdx.z * (16 * PASSES) + warp * 4 + (lane >> 3), n0 = V * (lane & 7);
   const int g = h / (a.H / a.G);
-  const int slot = seq_slot(a.q, s, tid, kTokThreads, [](bool t) { return __syncthreads_or(t) != 0; });
-  if (slot < 0) return;
-  const bool fresh = a.q.fresh && a.q.fresh[s];
-  TS* sp = static_cast<TS*>(a.state) + (size_t(slot) * a.H + h) * a.P * a.N;
-  float st[PASSES][NJ][4];
+  const int own = a.q.slot ? a.q.slot[s] : s;
+  const bool fresh = a.q.fresh && a.q.fresh[s], in = own >= 0 && own < a.q.n_slots;
+  TS* sp = static_cast<TS*>(a.state) + (size_t(in ? own : 0) * a.H + h) * a.P * a.N;
+  float st[PASSES][NJ][V];
 #pragma unroll
   for (int k = 0; k < PASSES; ++k)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int p = p0 + 16 * k, n = n0 + 32 * j;
-      if (!fresh && p < a.P && n < a.N) {
-        ldv<4>(sp + size_t(p) * a.N + n, st[k][j]);
-      } else {
+      const int p = p0 + 16 * k, n = n0 + 8 * V * j;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st[k][j][i] = 0.f;
-      }
+      for (int i = 0; i < V; ++i) st[k][j][i] = 0.f;
+      if (in && !fresh && p < a.P && n < a.N) ldv<V>(sp + size_t(p) * a.N + n, st[k][j]);
     }
   const TX* xr = static_cast<const TX*>(a.x.p) + s * a.x.stride + h * a.P;
   const TX* br = static_cast<const TX*>(a.B.p) + s * a.B.stride + g * a.N;
   const TX* cr = static_cast<const TX*>(a.C.p) + s * a.C.stride + g * a.N;
-  float bv[NJ][4], cv[NJ][4];
+  float bv[NJ][V], cv[NJ][V];
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + 32 * j + i;
-      bv[j][i] = n < a.N ? ldf(br + n) : 0.f;
-      cv[j][i] = n < a.N ? ldf(cr + n) : 0.f;
+    for (int i = 0; i < V; i += 4) {
+      const int n = n0 + 8 * V * j + i;
+      float* b4 = &bv[j][i];
+      float* c4 = &cv[j][i];
+      if (n < a.N && a.vec) {
+        ldv<4>(br + n, reinterpret_cast<float(&)[4]>(*b4));
+        ldv<4>(cr + n, reinterpret_cast<float(&)[4]>(*c4));
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          b4[u] = n < a.N ? ldf(br + n + u) : 0.f;
+          c4[u] = n < a.N ? ldf(cr + n + u) : 0.f;
+        }
+      }
     }
   const float dt = scan_dt(a, s, h), dA = expf(-dt * expf(a.A_log[h])), Dh = a.D ? a.D[h] : 0.f;
+  if (seq_slot(a.q, s, tid, kTokThreads, [](bool t) { return __syncthreads_or(t) != 0; }) < 0) return;
 #pragma unroll
   for (int k = 0; k < PASSES; ++k) {
     const int p = p0 + 16 * k;
@@ -394,12 +429,12 @@ __global__ void __launch_bounds__(kTokThreads) k_scan_token(ScanArgs a) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < V; ++i) {
         st[k][j][i] = fmaf(st[k][j][i], dA, u * bv[j][i]);
         y = fmaf(st[k][j][i], cv[j][i], y);
       }
-      const int n = n0 + 32 * j;
-      if (p < a.P && n < a.N) stv<4>(sp + size_t(p) * a.N + n, st[k][j]);
+      const int n = n0 + 8 * V * j;
+      if (p < a.P && n < a.N) stv<V>(sp + size_t(p) * a.N + n, st[k][j]);
     }
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
@@ -423,15 +458,9 @@ struct SegWork {
   int k, count;      // place among the sequence's segments
 };
 
-// The segment with number i, or false if no sequence has it.
+// The segment with number i, or false if no sequence has it (by converged warps).
 DFSSM_DEV bool seg_find(const ScanArgs& a, int i, SegWork& w) {
-  int lo = 0, hi = a.q.n_seqs;              // first s with seg_first(s) > i
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seg_first(a, mid, a.q.start[mid]) <= i) lo = mid + 1;
-    else hi = mid;
-  }
-  w.s = lo - 1;
+  w.s = warp_first(a.q.n_seqs, [&](int s) { return seg_first(a, s, a.q.start[s]) > i; }) - 1;
   if (w.s < 0) return false;
   if (!seq_rows(a.q, w.s, w.b, w.e)) {
     if (threadIdx.x == 0 && a.q.status) atomicOr(a.q.status, kSeqBadStart);

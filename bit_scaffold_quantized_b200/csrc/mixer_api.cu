@@ -196,6 +196,7 @@ ScanArgs scan_args(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* d
   a.q = dev_seqs(seqs);
   a.x = dev_rows(x); a.dt = dev_rows(dt); a.B = dev_rows(B); a.C = dev_rows(C); a.y = dev_rows(y);
   a.H = s->nheads; a.P = s->headdim; a.N = s->d_state; a.G = s->ngroups; a.dt16 = dt->dtype == DFSSM_DTYPE_F16;
+  a.vec = rows_in_pieces(B, 4) && rows_in_pieces(C, 4);
   a.dt_bias = s->dt_bias; a.A_log = s->A_log; a.D = s->D; a.state = state;
   return a;
 }
@@ -206,16 +207,22 @@ int scan_token_launch(const ScanArgs& a, cudaStream_t st) {
   const bool few = (long long)a.q.n_seqs * a.H * a.P <= 16LL * 4 * 4 * sm_count();
   const int rows = few ? 16 : 64;
   const dim3 grid(a.q.n_seqs, a.H, (a.P + rows - 1) / rows);
-  auto go = [&](auto nj) {
-    constexpr int NJ = decltype(nj)::value;
-    if (few) CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, NJ, 1>, grid, dim3(kTokThreads), 0, st, 0, a);
-    else CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, NJ, 4>, grid, dim3(kTokThreads), 0, st, 0, a);
+  auto go = [&](auto v, auto nj) {
+    constexpr int V = decltype(v)::value, NJ = decltype(nj)::value;
+    if (few) CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, V, NJ, 1>, grid, dim3(kTokThreads), 0, st, 0, a);
+    else CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, V, NJ, 4>, grid, dim3(kTokThreads), 0, st, 0, a);
     return int(DFSSM_OK);
   };
-  if (a.N <= 32) return go(std::integral_constant<int, 1>{});
-  if (a.N <= 64) return go(std::integral_constant<int, 2>{});
-  if (a.N <= 128) return go(std::integral_constant<int, 4>{});
-  return go(std::integral_constant<int, 8>{});
+  auto by_width = [&](auto v) {
+    constexpr int row = 8 * decltype(v)::value;       // values that eight lanes take at a time
+    if (a.N <= row) return go(v, std::integral_constant<int, 1>{});
+    if (a.N <= 2 * row) return go(v, std::integral_constant<int, 2>{});
+    if (a.N <= 4 * row) return go(v, std::integral_constant<int, 4>{});
+    return go(v, std::integral_constant<int, 256 / row>{});
+  };
+  if constexpr (sizeof(TS) == 2)
+    if (a.N % 8 == 0) return by_width(std::integral_constant<int, 8>{});
+  return by_width(std::integral_constant<int, 4>{});
 }
 
 // Blocks that share a head's state in k_scan_join: as many as there are values for while

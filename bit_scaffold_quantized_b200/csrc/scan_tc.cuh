@@ -76,11 +76,6 @@ DFSSM_DEV void umma_f16_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc, 
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
       :: "r"(d), "r"(a), "l"(bd), "r"(idesc), "r"(uint32_t(acc)) : "memory");
 }
-DFSSM_DEV float exp2_f(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 DFSSM_DEV float pow2_f(int k) { return __int_as_float((k + 127) << 23); }       // |k| <= 126
 // k with v 2^k in [2^13, 2^14) (0 for v = 0, and within [-80, 80]).
 DFSSM_DEV int scale_of(float v) {

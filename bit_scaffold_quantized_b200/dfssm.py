@@ -451,70 +451,68 @@ def df_decode(cells, lo, span, rows, stream=None) -> None:
 _ROWS = _struct.Struct("@Pqi4x").pack
 _SEQS = _struct.Struct("@iii4xPPPP").pack
 _SCAN = _struct.Struct("@iiiii4xPPP").pack
-_TYPES = {}
+_TYPES: dict = {}
 
 
-def _types():
+def _init_types() -> dict:
     import torch
-    _TYPES.update({torch.float16: DTYPE_F16, torch.float32: DTYPE_F32})
+    _TYPES.update({torch.float16: DTYPE_F16, torch.float32: DTYPE_F32, "f16": torch.float16, "f32": torch.float32,
+                   "i32": torch.int32, "device": torch._C._cuda_getDevice, "stream": torch._C._cuda_getCurrentRawStream})
     return _TYPES
 
 
 def _rows(t, name: str, n: int, width: int) -> bytes:
     """dfssm_rows of a 2-D tensor view [n, width] whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [{n}, {width}] with contiguous rows, not {tuple(t.shape)} with strides "
-                         f"{t.stride()}")
-    dtype = (_TYPES or _types()).get(t.dtype)
-    if dtype is None:
-        raise ValueError(f"{name}: {t.dtype} is neither float16 nor float32")
-    return _ROWS(t.data_ptr(), max(t.stride(0), width) if n <= 1 else t.stride(0), dtype)
+    step = t.stride()
+    dtype = _TYPES.get(t.dtype) if _TYPES else _init_types().get(t.dtype)
+    if t.shape != (n, width) or (step[1] != 1 and width > 1) or dtype is None:
+        raise ValueError(f"{name} must be float16 or float32 [{n}, {width}] with contiguous rows, not {t.dtype} "
+                         f"{tuple(t.shape)} with strides {step}")
+    return _ROWS(t.data_ptr(), step[0] if n > 1 else max(step[0], width), dtype)
 
 
-def _at(t, name: str, dtype, *shape) -> int:
+def _at(t, name: str, dtype: str, *shape) -> int:
     """Address of a contiguous tensor of this type and shape; 0 for None."""
     if t is None:
         return 0
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, not {t.dtype} "
+    if t.dtype is not (_TYPES or _init_types())[dtype] or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {_TYPES[dtype]} tensor of shape {shape}, not {t.dtype} "
                          f"{tuple(t.shape)} with strides {t.stride()}")
     return t.data_ptr()
 
 
 def _seqs(n_rows: int, start, slot, fresh, status, slots: int) -> bytes:
-    import torch
-    i32 = torch.int32
     n = n_rows if start is None else start.shape[0] - 1
     if n < 0:
         raise ValueError("start must hold one more entry than there are sequences")
-    return _SEQS(n, n_rows, slots, _at(start, "start", i32, n + 1), _at(slot, "slot", i32, n),
-                 _at(fresh, "fresh", i32, n), 0 if status is None else _at(status, "status", i32, 1))
+    return _SEQS(n, n_rows, slots, _at(start, "start", "i32", n + 1), _at(slot, "slot", "i32", n),
+                 _at(fresh, "fresh", "i32", n), _at(status, "status", "i32", 1))
 
 
 def _call(fn, tensors, stream, *args) -> None:
     """fn(*args, stream) on the device that all the tensors lie on."""
-    import torch
     dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
-            raise ValueError("all tensors must lie on one CUDA device")
-    if dev != torch.cuda.current_device():
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        raise ValueError("all tensors must lie on one CUDA device")
+    if dev != _TYPES["device"]():
+        import torch
         with torch.cuda.device(dev):
             return _call(fn, tensors, stream, *args)
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    rc = fn(*args, raw)
+    rc = fn(*args, _TYPES["stream"](dev) if stream is None else stream.cuda_stream)
     if rc != OK:
         raise DfssmError(rc, last_error())
 
 
 def _conv(fn, x, w, b, state, y, start, slot, fresh, silu, status, stream) -> None:
-    import torch
     n, c = x.shape
     width = w.shape[1]
     slots = 0 if state is None else state.shape[0]
     _call(fn, (x, w, b, state, y, start, slot, fresh, status), stream, c, width, int(silu), _rows(x, "x", n, c),
-          _at(w, "w", torch.float16, c, width), _at(b, "b", torch.float16, c),
-          _seqs(n, start, slot, fresh, status, slots), _at(state, "state", torch.float32, slots, width - 1, c),
+          _at(w, "w", "f16", c, width), _at(b, "b", "f16", c),
+          _seqs(n, start, slot, fresh, status, slots), _at(state, "state", "f32", slots, width - 1, c),
           _rows(y, "y", n, c))
 
 
@@ -531,19 +529,22 @@ def conv_token(x, w, b, state, y, slot=None, fresh=None, silu=True, status=None,
     _conv(lib().dfssm_conv_token, x, w, b, state, y, None, slot, fresh, silu, status, stream)
 
 
-def _scan_struct(x, B, dt_bias, A_log, D, state, headdim, groups) -> Tuple[bytes, int, int]:
-    import torch
+def _scan_struct(B, dt_bias, A_log, D, state, headdim, groups) -> Tuple[bytes, int, int, int]:
+    """dfssm_scan, and the widths of x and B and the number of slots."""
     H = dt_bias.shape[0]
+    dtype, slots = DTYPE_F32, 0
     if state is not None:
-        P, N = state.shape[2], state.shape[3]
+        slots, heads, P, N = state.shape
+        dtype = (_TYPES or _init_types()).get(state.dtype)
+        if dtype is None or heads != H or not state.is_contiguous():
+            raise ValueError("state must be a contiguous fp32 or fp16 tensor [slots, heads, headdim, d_state]")
         groups = B.shape[1] // max(N, 1)
     elif headdim and groups:
         P, N = headdim, B.shape[1] // groups
     else:
         raise ValueError("without a state, headdim and groups must be given")
-    f32 = torch.float32
-    return _SCAN(H, P, N, groups, DTYPE_F16 if state is not None and state.dtype == torch.float16 else DTYPE_F32,
-                 _at(dt_bias, "dt_bias", f32, H), _at(A_log, "A_log", f32, H), _at(D, "D", f32, H)), H * P, groups * N
+    return (_SCAN(H, P, N, groups, dtype, _at(dt_bias, "dt_bias", "f32", H), _at(A_log, "A_log", "f32", H),
+                  _at(D, "D", "f32", H)), H * P, groups * N, slots)
 
 
 def scan_workspace_bytes(nheads: int, headdim: int, d_state: int, groups: int, n_seqs: int, n_rows: int,
@@ -565,12 +566,7 @@ def scan_workspace(x, state, n_seqs: int, groups: int = 1):
 
 def _scan(fn, x, dt, B, Cm, dt_bias, A_log, D, state, y, start, slot, fresh, status, stream, ws, headdim, groups):
     n = x.shape[0]
-    s, E, GN = _scan_struct(x, B, dt_bias, A_log, D, state, headdim, groups)
-    slots = 0
-    if state is not None:
-        slots = state.shape[0]
-        if not state.is_contiguous() or state.dtype not in (_TYPES or _types()) or state.shape[1] != dt_bias.shape[0]:
-            raise ValueError("state must be a contiguous fp32 or fp16 tensor [slots, heads, headdim, d_state]")
+    s, E, GN, slots = _scan_struct(B, dt_bias, A_log, D, state, headdim, groups)
     args = (s, _rows(x, "x", n, E), _rows(dt, "dt", n, dt_bias.shape[0]), _rows(B, "B", n, GN), _rows(Cm, "C", n, GN),
             _seqs(n, start, slot, fresh, status, slots), _ptr(state), _rows(y, "y", n, E))
     if ws is not None:
@@ -598,21 +594,18 @@ def scan_token(x, dt, B, C, dt_bias, A_log, D, state, y, slot=None, fresh=None, 
 def gated_norm(y, z, w, out, groups: int = 1, stream=None) -> None:
     """out = rmsnorm(y * silu(z)) * w over each of `groups` parts of a row (dfssm_gated_norm);
     z None: no gate.  y, z, out [rows, cols] fp16 or fp32, w fp16 [cols]."""
-    import torch
     n, c = y.shape
     _call(lib().dfssm_gated_norm, (y, z, w, out), stream, n, c, groups, _rows(y, "y", n, c),
-          None if z is None else _rows(z, "z", n, c), _at(w, "w", torch.float16, c), _rows(out, "out", n, c))
+          None if z is None else _rows(z, "z", n, c), _at(w, "w", "f16", c), _rows(out, "out", n, c))
 
 
 def dense_forward(w, x, y, bias=None, residual=None, silu=False, status=None, stream=None) -> None:
     """y = act(x w^T + bias) + residual (dfssm_dense_forward): w fp16 [rows, cols], x fp16
     [batch, cols], bias fp16 [rows] or None, y and residual fp16 or fp32 [batch, rows]; y may be the
     residual itself."""
-    import torch
     rows, cols = w.shape
     n = x.shape[0]
-    f16 = torch.float16
-    _call(lib().dfssm_dense_forward, (x, w, bias, residual, y, status), stream, rows, cols, n, _at(w, "w", f16, rows, cols),
-          _at(bias, "bias", f16, rows), int(silu), _rows(x, "x", n, cols),
+    _call(lib().dfssm_dense_forward, (x, w, bias, residual, y, status), stream, rows, cols, n, _at(w, "w", "f16", rows, cols),
+          _at(bias, "bias", "f16", rows), int(silu), _rows(x, "x", n, cols),
           None if residual is None else _rows(residual, "residual", n, rows), _rows(y, "y", n, rows),
-          _at(status, "status", torch.int32, 1))
+          _at(status, "status", "i32", 1))
