@@ -3,6 +3,8 @@
 // with the running decay exponents in fp64; formulas and rules: dfssm.h.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace dfssm {
@@ -27,6 +29,22 @@ DFSSM_DEV float ldf(const float* p) { return *p; }
 DFSSM_DEV float ldf(const __half* p) { return __half2float(*p); }
 DFSSM_DEV void stf(float* p, float v) { *p = v; }
 DFSSM_DEV void stf(__half* p, float v) { *p = __float2half_rn(v); }
+
+// V values in registers, as they lie in memory, to floats.
+template <int V>
+DFSSM_DEV void unpack(const float* p, float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = p[i];
+}
+template <int V>
+DFSSM_DEV void unpack(const __half* p, float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(p + i));
+    v[i] = f.x;
+    v[i + 1] = f.y;
+  }
+}
 
 // VEC consecutive values; VEC > 1 needs the address aligned to VEC values.
 template <int VEC>
@@ -87,6 +105,17 @@ DFSSM_DEV void stv(__half* p, const float (&v)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) p[i] = __float2half_rn(v[i]);
   }
+}
+
+// Two fp32 operations in one instruction.
+DFSSM_DEV void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+DFSSM_DEV void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
 
 // 2^v, 2 ulp, flushing subnormal results.
@@ -172,16 +201,21 @@ struct ConvArgs {
 
 constexpr int kConvThreads = 128;
 constexpr int kConvTile = 32;       // rows of one block
-constexpr int kConvUnroll = 8;      // rows loaded ahead
+constexpr int kConvUnroll = 4;      // rows loaded ahead
 
 template <int VEC, int W>
 DFSSM_DEV void conv_weights(const ConvArgs& a, int c, float (&w)[W][VEC], float (&bias)[VEC]) {
+  const __half* wp = reinterpret_cast<const __half*>(a.w) + size_t(c) * W;
+  float f[VEC * W];
+#pragma unroll
+  for (int i = 0; i < VEC * W; i += VEC) ldv<VEC>(wp + i, reinterpret_cast<float(&)[VEC]>(f[i]));
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
+    bias[i] = 0.f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = h2f(a.w[size_t(c + i) * W + j]);
-    bias[i] = a.b ? h2f(a.b[c + i]) : 0.f;
+    for (int j = 0; j < W; ++j) w[j][i] = f[i * W + j];
   }
+  if (a.b) ldv<VEC>(reinterpret_cast<const __half*>(a.b) + c, bias);
 }
 
 template <int VEC, int W>
@@ -213,7 +247,7 @@ DFSSM_DEV int conv_edge(const Seqs& q, int t) {
 // One block: kConvTile rows of kConvThreads * VEC channels; a thread walks its channels
 // down the rows with the last W - 1 inputs in registers.
 template <typename TX, typename TY, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads) k_conv_prompt(ConvArgs a) {
+__global__ void __launch_bounds__(kConvThreads, 7) k_conv_prompt(ConvArgs a) {
   pdl_wait();
   pdl_release();
   const int tile = blockIdx.x / a.cblocks, lane = threadIdx.x & 31;
@@ -372,30 +406,33 @@ DFSSM_DEV float scan_dt(const ScanArgs& a, long long row, int h) { return softpl
 
 constexpr int kTokThreads = 128;
 
-// One token: block = (sequence, head, PASSES * 16 rows of the head's state).  Eight lanes
-// share a state row, V consecutive values (16 bytes; 8 for fp16 rows that are no multiple of
-// 16) each, NJ times; a warp has four rows.
-// Nothing but the state's own bytes counts: all of a thread's are asked for at once, before
-// the look at the earlier sequences' slots.
-template <typename TX, typename TY, typename TS, int V, int NJ, int PASSES>
-__global__ void __launch_bounds__(kTokThreads) k_scan_token(ScanArgs a) {
+// One token: block = (sequence, head, PASSES * 128 / LANES rows of the head's state).  (Numbered
+// in the order of the state's memory instead, sequences last, it takes a fifth longer.)
+// LANES lanes share a state row, V consecutive values (16 bytes; 8 for fp16 rows that are no
+// multiple of 16) each, NJ times.  Nothing but the state's own bytes counts: all of a thread's
+// are asked for at once, before the look at the earlier sequences' slots, and wait in
+// registers as they lie in memory.  128 sequences of the 64-head layer, fp16 states: 64 us
+// with eight lanes a row (whose shares of B and C spilled), 71 us with unpacked states.
+template <typename TX, typename TY, typename TS, int V, int LANES, int NJ, int PASSES>
+__global__ void __launch_bounds__(kTokThreads, V * NJ <= 8 ? 6 : 4) k_scan_token(ScanArgs a) {
   pdl_wait();
   pdl_release();
   const int s = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int p0 = blockIdx.z * (16 * PASSES) + warp * 4 + (lane >> 3), n0 = V * (lane & 7);
+  constexpr int ROWS = kTokThreads / LANES;            // of a pass
+  const int p0 = blockIdx.z * (ROWS * PASSES) + tid / LANES, n0 = V * (lane % LANES);
   const int g = h / (a.H / a.G);
   const int own = a.q.slot ? a.q.slot[s] : s;
   const bool fresh = a.q.fresh && a.q.fresh[s], in = own >= 0 && own < a.q.n_slots;
   TS* sp = static_cast<TS*>(a.state) + (size_t(in ? own : 0) * a.H + h) * a.P * a.N;
-  float st[PASSES][NJ][V];
+  using Raw = std::conditional_t<V * sizeof(TS) == 16, uint4, uint2>;      // as it lies in memory: half the
+  Raw st[PASSES][NJ];                                                        // registers where it is fp16
 #pragma unroll
   for (int k = 0; k < PASSES; ++k)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int p = p0 + 16 * k, n = n0 + 8 * V * j;
-#pragma unroll
-      for (int i = 0; i < V; ++i) st[k][j][i] = 0.f;
-      if (in && !fresh && p < a.P && n < a.N) ldv<V>(sp + size_t(p) * a.N + n, st[k][j]);
+      const int p = p0 + ROWS * k, n = n0 + LANES * V * j;
+      st[k][j] = Raw{};
+      if (in && !fresh && p < a.P && n < a.N) st[k][j] = *reinterpret_cast<const Raw*>(sp + size_t(p) * a.N + n);
     }
   const TX* xr = static_cast<const TX*>(a.x.p) + s * a.x.stride + h * a.P;
   const TX* br = static_cast<const TX*>(a.B.p) + s * a.B.stride + g * a.N;
@@ -405,7 +442,7 @@ __global__ void __launch_bounds__(kTokThreads) k_scan_token(ScanArgs a) {
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-      const int n = n0 + 8 * V * j + i;
+      const int n = n0 + LANES * V * j + i;
       float* b4 = &bv[j][i];
       float* c4 = &cv[j][i];
       if (n < a.N && a.vec) {
@@ -419,26 +456,41 @@ __global__ void __launch_bounds__(kTokThreads) k_scan_token(ScanArgs a) {
         }
       }
     }
-  const float dt = scan_dt(a, s, h), dA = expf(-dt * expf(a.A_log[h])), Dh = a.D ? a.D[h] : 0.f;
+  __shared__ float step[2];
+  if (warp == 0) {              // the other warps need not repeat it
+    const float dt = scan_dt(a, s, h), dA = expf(-dt * expf(a.A_log[h]));
+    if (lane == 0) {
+      step[0] = dt;
+      step[1] = dA;
+    }
+  }
+  const float Dh = a.D ? a.D[h] : 0.f;
+  __syncthreads();
+  const float dt = step[0], dA = step[1];
   if (seq_slot(a.q, s, tid, kTokThreads, [](bool t) { return __syncthreads_or(t) != 0; }) < 0) return;
 #pragma unroll
   for (int k = 0; k < PASSES; ++k) {
-    const int p = p0 + 16 * k;
+    const int p = p0 + ROWS * k;
     const float x = p < a.P ? ldf(xr + p) : 0.f, u = dt * x;
-    float y = 0.f;
+    float y0 = 0.f, y1 = 0.f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
+      float t[V];
+      unpack(reinterpret_cast<const TS*>(&st[k][j]), t);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        st[k][j][i] = fmaf(st[k][j][i], dA, u * bv[j][i]);
-        y = fmaf(st[k][j][i], cv[j][i], y);
+      for (int i = 0; i < V; i += 2) {
+        float w0, w1;
+        mul2(w0, w1, u, u, bv[j][i], bv[j][i + 1]);
+        fma2(t[i], t[i + 1], t[i], t[i + 1], dA, dA, w0, w1);
+        fma2(y0, y1, t[i], t[i + 1], cv[j][i], cv[j][i + 1], y0, y1);
       }
-      const int n = n0 + 8 * V * j;
-      if (p < a.P && n < a.N) stv<V>(sp + size_t(p) * a.N + n, st[k][j]);
+      const int n = n0 + LANES * V * j;
+      if (p < a.P && n < a.N) stv<V>(sp + size_t(p) * a.N + n, t);
     }
+    float y = y0 + y1;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if ((lane & 7) == 0 && p < a.P)
+    for (int o = LANES / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    if (lane % LANES == 0 && p < a.P)
       stf(static_cast<TY*>(a.y.p) + s * a.y.stride + h * a.P + p, fmaf(Dh, x, y));
   }
 }

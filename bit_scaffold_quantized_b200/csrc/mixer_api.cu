@@ -203,22 +203,25 @@ ScanArgs scan_args(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* d
 
 template <typename TX, typename TY, typename TS>
 int scan_token_launch(const ScanArgs& a, cudaStream_t st) {
-  // one pass of 16 state rows per block while there are few blocks, four from there on
+  // one pass per block while there are few blocks (latency counts), else about 128 bytes of
+  // state per thread
   const bool few = (long long)a.q.n_seqs * a.H * a.P <= 16LL * 4 * 4 * sm_count();
-  const int rows = few ? 16 : 64;
-  const dim3 grid(a.q.n_seqs, a.H, (a.P + rows - 1) / rows);
-  auto go = [&](auto v, auto nj) {
-    constexpr int V = decltype(v)::value, NJ = decltype(nj)::value;
-    if (few) CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, V, NJ, 1>, grid, dim3(kTokThreads), 0, st, 0, a);
-    else CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, V, NJ, 4>, grid, dim3(kTokThreads), 0, st, 0, a);
+  auto go = [&](auto v, auto lanes, auto nj) {
+    constexpr int V = decltype(v)::value, L = decltype(lanes)::value, NJ = decltype(nj)::value;
+    constexpr int PASSES = L == 16 ? 8 / NJ : 4, ROWS = kTokThreads / L;
+    const int rows = few ? ROWS : ROWS * PASSES;
+    const dim3 grid(a.q.n_seqs, a.H, (a.P + rows - 1) / rows);
+    if (few) CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, V, L, NJ, 1>, grid, dim3(kTokThreads), 0, st, 0, a);
+    else CHAIN_LAUNCH("k_scan_token", k_scan_token<TX, TY, TS, V, L, NJ, PASSES>, grid, dim3(kTokThreads), 0, st, 0, a);
     return int(DFSSM_OK);
   };
   auto by_width = [&](auto v) {
-    constexpr int row = 8 * decltype(v)::value;       // values that eight lanes take at a time
-    if (a.N <= row) return go(v, std::integral_constant<int, 1>{});
-    if (a.N <= 2 * row) return go(v, std::integral_constant<int, 2>{});
-    if (a.N <= 4 * row) return go(v, std::integral_constant<int, 4>{});
-    return go(v, std::integral_constant<int, 256 / row>{});
+    constexpr int V = decltype(v)::value;
+    using std::integral_constant;
+    if (a.N <= 8 * V) return go(v, integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    if (a.N <= 16 * V) return go(v, integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    if (a.N <= 32 * V) return go(v, integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    return go(v, integral_constant<int, 16>{}, integral_constant<int, 256 / (16 * V)>{});
   };
   if constexpr (sizeof(TS) == 2)
     if (a.N % 8 == 0) return by_width(std::integral_constant<int, 8>{});
