@@ -83,7 +83,11 @@ int conv_launch(ConvArgs a, bool token, cudaStream_t st) {
     return DFSSM_OK;
   }
   a.cblocks = cblocks;
-  const long long blocks = (long long)cblocks * ((a.q.n_rows + kConvTile - 1) / kConvTile);
+  // tiles of at most kConvTile rows, in whole waves of resident blocks
+  const long long slots = (long long)kConvBlocks * sm_count(), work = (long long)a.q.n_rows * cblocks;
+  const long long waves = (work + slots * kConvTile - 1) / (slots * kConvTile);
+  a.tile = int(std::max<long long>(8, (work + slots * waves - 1) / (slots * waves)));
+  const long long blocks = (long long)cblocks * ((a.q.n_rows + a.tile - 1) / a.tile);
   REQUIRE(blocks <= INT_MAX, DFSSM_ERR_UNSUPPORTED_SHAPE, "n_rows (%d) x channels (%d) out of range", a.q.n_rows, a.channels);
   CHAIN_LAUNCH("k_conv_prompt", k_conv_prompt<TX, TY, VEC, W>, dim3(unsigned(blocks)), dim3(kConvThreads), 0, st, 0, a);
   return DFSSM_OK;
