@@ -125,6 +125,20 @@ DFSSM_DEV float exp2_f(float v) {
   return r;
 }
 
+DFSSM_DEV float pow2_f(int k) { return __int_as_float((k + 127) << 23); }       // |k| <= 126
+// k with v 2^k in [2^13, 2^14) (0 for v = 0, and within [-80, 80]).
+DFSSM_DEV int scale_of(float v) {
+  const int e = int((__float_as_uint(v) >> 23) & 0xffu) - 126;                    // v < 2^e
+  return v > 0.f ? max(-80, min(80, 14 - e)) : 0;
+}
+// Two values as fp16 pieces: hi = their fp16 pair, lo that of what is left.
+DFSSM_DEV void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const float2 f = __half22float2(h);
+  lo = pack_h2(a - f.x, b - f.y);
+}
+
 // v / (1 + e^-v) in five instructions: the rounding of v log2 e and the two approximate
 // steps leave it within (|v| + 4) 2^-24 of itself.  With expf and its range reduction the conv
 // and the norm were bound by instructions, not memory.
@@ -384,7 +398,7 @@ struct ScanArgs {
   Seqs q;
   Rows x, dt, B, C, y;
   int H, P, N, G, dt16;
-  int vec;               // rows of B and C can be read four values at a time
+  int vec, vecx;         // rows of B and C, rows of x can be read four values at a time
   const float* dt_bias;
   const float* A_log;
   const float* D;
@@ -537,7 +551,8 @@ __host__ __device__ constexpr size_t scan_smem_bytes(int P, int N) {
                            size_t(kScanQ) * (kScanQ + 4) + 3 * kScanQ);
 }
 
-// Any shape and type.  Block = (segment, head), the segment in chunks of Q = 32 rows
+// The shapes that k_scan_mma does not hold (heads of more than 64, more than 128 states).
+// Block = (segment, head), the segment in chunks of Q = 32 rows
 // with the head's state in shared memory: with cs_t the running sum of -dt exp(A_log),
 //   y_t = sum_{s <= t} (C_t . B_s) exp(cs_t - cs_s) dt_s x_s + exp(cs_t) C_t . state + D x_t,
 //   state <- exp(cs_Q) state + sum_s exp(cs_Q - cs_s) dt_s x_s (x) B_s.

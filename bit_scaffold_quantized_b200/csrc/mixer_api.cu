@@ -8,6 +8,7 @@
 #include "dfssm.h"
 #include "host.cuh"
 #include "mixer.cuh"
+#include "scan_mma.cuh"
 #include "scan_tc.cuh"
 
 using namespace dfssm;
@@ -144,6 +145,8 @@ int check_scan(const dfssm_scan* s) {
 // Whether the prompt form runs on the tensor cores (k_scan_tc): fp16 rows of heads of 64
 // with 64 or 128 states, heads in pairs of one group.  (The rows' alignment decides at the
 // call: the workspace is large enough for either.)
+enum ScanPath { kScanSimt, kScanMma, kScanTc };
+
 bool scan_tc_shape(const dfssm_scan* s, int dtype) {
   return dtype == DFSSM_DTYPE_F16 && s->headdim == kStP && (s->d_state == 64 || s->d_state == 128) &&
          s->nheads / s->ngroups % 2 == 0;
@@ -157,10 +160,14 @@ struct ScanPlan {
   size_t decay_at, rec_at, big_at, bytes;
 };
 
-ScanPlan scan_plan(const dfssm_scan* s, bool tc, int n_seqs, int n_rows) {
+// Heads of up to 64 with up to 128 states run on mma.sync otherwise, larger ones on FMAs.
+ScanPath scan_other_path(const dfssm_scan* s) { return s->headdim <= kSmP && s->d_state <= 128 ? kScanMma : kScanSimt; }
+
+ScanPlan scan_plan(const dfssm_scan* s, ScanPath path, int n_seqs, int n_rows) {
   ScanPlan p;
-  const int unit = tc ? kStQ : kScanQ, heads = tc ? s->nheads / 2 : s->nheads;
-  const long long want = tc ? 2LL * sm_count() : 4LL * sm_count();
+  const bool tc = path == kScanTc;
+  const int unit = tc ? kStQ : path == kScanMma ? kSmQ : kScanQ, heads = tc ? s->nheads / 2 : s->nheads;
+  const long long want = tc ? 2LL * sm_count() : path == kScanMma ? 3LL * sm_count() : 4LL * sm_count();
   long long seg = ((long long)n_rows * heads + want - 1) / want;
   seg = std::max<long long>(tc ? 2 * kStQ : 4 * kScanQ, (seg + unit - 1) / unit * unit);
   p.seg = int(seg);
@@ -201,6 +208,7 @@ ScanArgs scan_args(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* d
   a.x = dev_rows(x); a.dt = dev_rows(dt); a.B = dev_rows(B); a.C = dev_rows(C); a.y = dev_rows(y);
   a.H = s->nheads; a.P = s->headdim; a.N = s->d_state; a.G = s->ngroups; a.dt16 = dt->dtype == DFSSM_DTYPE_F16;
   a.vec = rows_in_pieces(B, 4) && rows_in_pieces(C, 4);
+  a.vecx = rows_in_pieces(x, 4);
   a.dt_bias = s->dt_bias; a.A_log = s->A_log; a.D = s->D; a.state = state;
   return a;
 }
@@ -255,6 +263,31 @@ int scan_prompt_launch(const ScanArgs& a, cudaStream_t st) {
   }
   CHAIN_LAUNCH("k_scan_prompt", k_scan_prompt<TX, TY, TS, false>, grid, dim3(kScanThreads), smem, st, 0, a);
   return DFSSM_OK;
+}
+
+template <typename TX, typename TY, typename TS, int NP>
+int scan_mma_launch(const ScanArgs& a, cudaStream_t st) {
+  constexpr int pieces = sizeof(TX) == 4 ? 2 : 1;
+  constexpr size_t smem = sm_smem_bytes(NP, pieces, false), states = sm_smem_bytes(NP, pieces, true);
+  const auto kernel = k_scan_mma<TX, TY, TS, NP, false>;
+  const auto before = k_scan_mma<TX, float, float, NP, true>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(before, cudaFuncAttributeMaxDynamicSharedMemorySize, int(states));
+  if (e != cudaSuccess) return fail(DFSSM_ERR_CUDA, "k_scan_mma smem attribute: %s", cudaGetErrorString(e));
+  const dim3 grid(a.max_segs, a.H);
+  if (a.seg_state) {
+    CHAIN_LAUNCH("k_scan_mma", before, grid, dim3(kSmThreads), states, st, 0, a);
+    CHAIN_LAUNCH("k_scan_join", k_scan_join<TS>, dim3(a.q.n_seqs, a.H, join_blocks(a)), dim3(256), 0, st, 0, a);
+  }
+  CHAIN_LAUNCH("k_scan_mma", kernel, grid, dim3(kSmThreads), smem, st, 0, a);
+  return DFSSM_OK;
+}
+
+template <typename TX, typename TY, typename TS>
+int scan_mma_shape(const ScanArgs& a, cudaStream_t st) {
+  if (a.N <= 16) return scan_mma_launch<TX, TY, TS, 16>(a, st);
+  if (a.N <= 64) return scan_mma_launch<TX, TY, TS, 64>(a, st);
+  return scan_mma_launch<TX, TY, TS, 128>(a, st);
 }
 
 int scan_map(CUtensorMap* map, const Rows& r, long long cols, int n_rows) {
@@ -467,8 +500,8 @@ size_t dfssm_scan_workspace_bytes(const dfssm_scan* s, int dtype, int n_seqs, in
     return 0;
   }
   ok();
-  const size_t any = scan_plan(s, false, n_seqs, n_rows).bytes;
-  return std::max<size_t>({16, any, scan_tc_shape(s, dtype) ? scan_plan(s, true, n_seqs, n_rows).bytes : 0});
+  const size_t any = scan_plan(s, scan_other_path(s), n_seqs, n_rows).bytes;
+  return std::max<size_t>({16, any, scan_tc_shape(s, dtype) ? scan_plan(s, kScanTc, n_seqs, n_rows).bytes : 0});
 }
 
 int dfssm_scan_prompt(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* dt, const dfssm_rows* B,
@@ -483,7 +516,8 @@ int dfssm_scan_prompt(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows
   ScanArgs a = scan_args(s, x, dt, B, C, seqs, state, y);
   const bool tc = scan_tc_shape(s, x->dtype) && rows_in_pieces(x, 8) && rows_in_pieces(B, 8) && rows_in_pieces(C, 8) &&
                   rows_in_pieces(y, 8);
-  const ScanPlan p = scan_plan(s, tc, seqs->n_seqs, seqs->n_rows);
+  const ScanPath path = tc ? kScanTc : scan_other_path(s);
+  const ScanPlan p = scan_plan(s, path, seqs->n_seqs, seqs->n_rows);
   a.seg = p.seg;
   a.max_segs = p.max_segs;
   auto at = [&](size_t off) { return reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + off); };
@@ -505,8 +539,9 @@ int dfssm_scan_prompt(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows
   rc = by_types(x->dtype, y->dtype, [&](auto tx, auto ty) {
     using TX = decltype(tx);
     using TY = decltype(ty);
-    return s->state_dtype == DFSSM_DTYPE_F16 ? scan_prompt_launch<TX, TY, __half>(a, st)
-                                             : scan_prompt_launch<TX, TY, float>(a, st);
+    const bool half = s->state_dtype == DFSSM_DTYPE_F16;
+    if (path == kScanMma) return half ? scan_mma_shape<TX, TY, __half>(a, st) : scan_mma_shape<TX, TY, float>(a, st);
+    return half ? scan_prompt_launch<TX, TY, __half>(a, st) : scan_prompt_launch<TX, TY, float>(a, st);
   });
   return rc ? rc : ok();
 }

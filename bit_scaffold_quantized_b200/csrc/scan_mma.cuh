@@ -1,0 +1,378 @@
+// Selective scan over packed prompts on mma.sync: heads of up to 64 with up to 128 states,
+// fp32 or fp16 rows of any alignment.
+#pragma once
+
+#include "mixer.cuh"
+
+namespace dfssm {
+
+// One block: (segment, head), the segment in chunks of Q = 64 rows; the four products of a
+// chunk are those of k_scan_tc (Y1 = M X, Y2 = C H^T, S = W B, CB = C B^T), each on m16n8k16
+// fp16 products with fp32 accumulators:
+//   fp32 values go in as two fp16 pieces, value = hi + lo to 2^-22, scaled by a power of two
+//   (x, B and C by the chunk's largest, M, W and H by bounds) so that the largest lies below
+//   2^14, and three products hi hi + hi lo + lo hi; fp16 rows are exact in one piece.
+// 8 warps.  CB, Y1, Y2: warp = 16 rows t x half of the columns; S and H: warp = 16 rows p x
+// half of the columns n, H in registers (fp32) throughout.  The next chunk's rows are on
+// their way in registers meanwhile.
+// The legacy tensor path suffices: 1000 rows of the 64-head layer in fp32 take MMA_FIGURES.
+constexpr int kSmQ = 64, kSmP = 64, kSmThreads = 256;
+constexpr int kSmXS = kSmP + 8;          // row strides in halves: 16 bytes past a multiple of 128, so that
+                                          // ldmatrix's eight rows lie in different banks
+__host__ __device__ constexpr int sm_ns(int np) { return np + 8; }
+__host__ __device__ constexpr size_t sm_smem_bytes(int np, int pieces, bool states) {
+  return 2 * (size_t(pieces) * kSmQ * (sm_ns(np) * (states ? 1 : 2) + kSmXS) + 2 * kSmQ * kSmXS * (states ? 1 : 2) +
+              (states ? 0 : 2 * kSmP * sm_ns(np)));
+}
+
+DFSSM_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+DFSSM_DEV void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// Four values of row `row`, columns col .. col + 3, zero outside the row.
+template <typename T>
+DFSSM_DEV void load4(const Rows& r, long long row, int col, int width, bool vec, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = 0.f;
+  if (row < 0 || col >= width) return;          // widths are multiples of 4
+  const T* p = static_cast<const T*>(r.p) + row * r.stride + col;
+  if (vec) {
+    ldv<4>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ldf(p + i);
+  }
+}
+DFSSM_DEV float finite_top(float m, const float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(v[i]) < 3e38f ? fabsf(v[i]) : 0.f);
+  return m;
+}
+// Four values, scaled, as fp16 pieces at hi (and hi + lo_at).
+template <int PIECES>
+DFSSM_DEV void store4(__half* hi, int lo_at, const float (&v)[4], float up) {
+  uint32_t h[2], l[2];
+  split_h2(v[0] * up, v[1] * up, h[0], l[0]);
+  split_h2(v[2] * up, v[3] * up, h[1], l[1]);
+  *reinterpret_cast<uint2*>(hi) = make_uint2(h[0], h[1]);
+  if (PIECES == 2) *reinterpret_cast<uint2*>(hi + lo_at) = make_uint2(l[0], l[1]);
+}
+
+template <typename TX, typename TY, typename TS, int NP, bool STATES>
+__global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
+  pdl_wait();
+  pdl_release();
+  constexpr int PIECES = sizeof(TX) == 4 ? 2 : 1, SN = sm_ns(NP), Q = kSmQ;
+  constexpr int NT = NP / 16;                           // n tiles of a warp's half of the state
+  constexpr int GX = Q * kSmP / 4 / kSmThreads, GN = Q * NP / 4 / kSmThreads;      // groups of four per thread
+  extern __shared__ __align__(16) unsigned char sm_raw[];
+  __half* const Bs = reinterpret_cast<__half*>(sm_raw);             // [PIECES][Q][SN]
+  __half* const Xs = Bs + PIECES * Q * SN;                          // [PIECES][Q][kSmXS]
+  __half* const Ws = Xs + PIECES * Q * kSmXS;                       // [2][Q][kSmXS]
+  __half* const Ms = Ws + 2 * Q * kSmXS;                            // [2][Q][kSmXS]
+  __half* const Cs = Ms + 2 * Q * kSmXS;                            // [PIECES][Q][SN]
+  __half* const Hs = Cs + PIECES * Q * SN;                          // [2][kSmP][SN]
+  __shared__ float hi_s[Q], lo_s[Q], dt_s[Q], w_s[Q], red[4][8], sums[3];      // sums: exp(cs_Q), max dt, max w
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, t4 = lane & 3;
+  const int P = a.P, N = a.N, h = blockIdx.y, g = h / (a.H / a.G);
+  SegWork w;
+  if (!seg_find(a, blockIdx.x, w)) return;
+  if (STATES && w.k == w.count - 1) return;
+  int slot = -1;
+  if (a.state) {
+    slot = seq_slot(a.q, w.s, tid, kSmThreads, [](bool v) { return __syncthreads_or(v) != 0; });
+    if (slot < 0) return;
+  }
+  TS* const state = a.state ? static_cast<TS*>(a.state) + (size_t(slot) * a.H + h) * P * N : nullptr;
+  float* const seg_state = a.seg_state + (size_t(blockIdx.x) * a.H + h) * P * N;
+  const bool old = !STATES && w.count == 1 && state && !(a.q.fresh && a.q.fresh[w.s]);
+  const int r16 = 16 * (warp & 3), half = warp >> 2;    // the warp's rows (t or p), its half of the columns
+  const double rate = -exp(double(a.A_log[h])), log2e = 1.4426950408889634;
+  const float bias = a.dt_bias[h], Dh = a.D ? a.D[h] : 0.f;
+
+  // H: rows r16 + g4 (+ 8), columns half NP / 2 + 8 i + 2 t4 (+ 1)
+  float hs[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int p = r16 + g4 + 8 * (j >> 1), n = half * (NP / 2) + 8 * i + 2 * t4 + (j & 1);
+      hs[i][j] = 0.f;
+      if (!STATES && p < P && n < N) {
+        if (w.count > 1) hs[i][j] = seg_state[p * N + n];
+        else if (old) hs[i][j] = ldf(state + p * N + n);
+      }
+    }
+  float hup = 1.f;
+  auto top_of = [&](int which, float m) {       // the block's largest, after the next barrier: red_top(which)
+    m = warp_max(m);
+    if (lane == 0) red[which][warp] = m;
+  };
+  auto red_top = [&](int which) {
+    const float4 u = *reinterpret_cast<const float4*>(&red[which][0]), v = *reinterpret_cast<const float4*>(&red[which][4]);
+    return fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+  };
+  auto put_h = [&]() {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) m = finite_top(m, hs[i]);
+    top_of(3, m);
+    __syncthreads();
+    hup = pow2_f(scale_of(red_top(3)));
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        uint32_t hi, lo;
+        split_h2(hs[i][j] * hup, hs[i][j + 1] * hup, hi, lo);
+        __half* at = Hs + (r16 + g4 + 4 * j) * SN + half * (NP / 2) + 8 * i + 2 * t4;
+        *reinterpret_cast<uint32_t*>(at) = hi;
+        *reinterpret_cast<uint32_t*>(at + kSmP * SN) = lo;
+      }
+  };
+  if (!STATES) put_h();
+
+  float vx[GX][4], vb[GN][4], vc[STATES ? 1 : GN][4], raw[2];
+  auto fetch = [&](int t0) {
+    auto row = [&](int t) { return t0 + t < w.t1 ? (long long)(t0 + t) : -1LL; };
+#pragma unroll
+    for (int i = 0; i < GX; ++i) {
+      const int e = tid + i * kSmThreads, t = e / (kSmP / 4), c = 4 * (e % (kSmP / 4));
+      load4<TX>(Rows{static_cast<TX*>(a.x.p) + h * P, a.x.stride}, row(t), c, P, a.vecx != 0, vx[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < GN; ++i) {
+      const int e = tid + i * kSmThreads, t = e / (NP / 4), c = 4 * (e % (NP / 4));
+      load4<TX>(Rows{static_cast<TX*>(a.B.p) + g * N, a.B.stride}, row(t), c, N, a.vec != 0, vb[i]);
+      if (!STATES) load4<TX>(Rows{static_cast<TX*>(a.C.p) + g * N, a.C.stride}, row(t), c, N, a.vec != 0, vc[i]);
+    }
+    if (warp == 0)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) raw[j] = scan_raw(a, min(t0 + 2 * lane + j, w.t1 - 1), h);
+  };
+  fetch(w.t0);
+  double total_log2 = 0.0;
+  for (int t0 = w.t0; t0 < w.t1; t0 += Q) {
+    const int n = min(Q, w.t1 - t0);
+    // the largest of x, B, C; warp 0: steps, running sums, factors
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < GX; ++i) m = finite_top(m, vx[i]);
+    top_of(0, m);
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < GN; ++i) m = finite_top(m, vb[i]);
+    top_of(1, m);
+    if (!STATES) {
+      m = 0.f;
+#pragma unroll
+      for (int i = 0; i < GN; ++i) m = finite_top(m, vc[i]);
+      top_of(2, m);
+    }
+    if (warp == 0) {
+      float dt[2], wf[2];
+      double cs[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) dt[j] = 2 * lane + j < n ? softplus_f(raw[j] + bias) : 0.f;
+      cs[0] = double(dt[0]) * rate;
+      cs[1] = cs[0] + double(dt[1]) * rate;
+      double up = cs[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += v;
+      }
+      const double total = __shfl_sync(0xffffffffu, up, 31), before = up - cs[1];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        cs[j] += before;
+        const double e = cs[j] * log2e;
+        const float hi = float(e);
+        hi_s[2 * lane + j] = hi;
+        lo_s[2 * lane + j] = float(e - double(hi));
+        dt_s[2 * lane + j] = dt[j];
+        wf[j] = exp2_f(float((total - cs[j]) * log2e)) * dt[j];
+        w_s[2 * lane + j] = wf[j];
+      }
+      const float dmax = warp_max(fmaxf(dt[0], dt[1])), wmax = warp_max(fmaxf(wf[0], wf[1]));
+      total_log2 += total * log2e;
+      if (lane == 0) {
+        sums[0] = exp2_f(float(total * log2e));
+        sums[1] = dmax;
+        sums[2] = wmax;
+      }
+    }
+    __syncthreads();
+    const float xt = red_top(0), bt = red_top(1), ct = STATES ? 0.f : red_top(2), keep = sums[0];
+    const float xup = PIECES == 2 ? pow2_f(scale_of(xt)) : 1.f, bup = PIECES == 2 ? pow2_f(scale_of(bt)) : 1.f,
+                cup = PIECES == 2 ? pow2_f(scale_of(ct)) : 1.f;
+    const float wup = pow2_f(scale_of(xt * sums[2])), mup = pow2_f(scale_of(fmaf(float(NP) * bt * ct, sums[1], fabsf(Dh))));
+#pragma unroll
+    for (int i = 0; i < GX; ++i) {
+      const int e = tid + i * kSmThreads, t = e / (kSmP / 4), c = 4 * (e % (kSmP / 4));
+      if (!STATES) store4<PIECES>(Xs + t * kSmXS + c, Q * kSmXS, vx[i], xup);
+      store4<2>(Ws + t * kSmXS + c, Q * kSmXS, vx[i], w_s[t] * wup);
+    }
+#pragma unroll
+    for (int i = 0; i < GN; ++i) {
+      const int e = tid + i * kSmThreads, t = e / (NP / 4), c = 4 * (e % (NP / 4));
+      store4<PIECES>(Bs + t * SN + c, Q * SN, vb[i], bup);
+      if (!STATES) store4<PIECES>(Cs + t * SN + c, Q * SN, vc[i], cup);
+    }
+    if (t0 + Q < w.t1) fetch(t0 + Q);
+    __syncthreads();
+    const int arow = r16 + (lane & 15), acol = 8 * (lane >> 4);               // A as it lies
+    const int trow = (lane & 7) + 8 * (lane >> 4), tcol = 8 * ((lane >> 3) & 1);   // A transposed
+    const int brow = (lane & 7) + 8 * (lane >> 4), bcol = 8 * ((lane >> 3) & 1);   // B as it lies: rows n
+    const int krow = lane & 15, kcol = 8 * (lane >> 4);                       // B transposed: rows k
+    if (!STATES) {
+      // CB: rows t = r16 .., columns s = 32 half ..
+      float acc[4][4] = {};
+      if (32 * half <= r16 + 15) {
+        for (int k = 0; k < NP; k += 16) {
+          uint32_t ca[PIECES][4], b[PIECES][4];
+#pragma unroll
+          for (int u = 0; u < PIECES; ++u) ldsm4(ca[u], smem_u32(Cs + u * Q * SN + arow * SN + k + acol));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int u = 0; u < PIECES; ++u) ldsm4(b[u], smem_u32(Bs + u * Q * SN + (32 * half + 16 * j + brow) * SN + k + bcol));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              mma_f16_16816(acc[2 * j + i], ca[0], b[0][2 * i], b[0][2 * i + 1]);
+              if (PIECES == 2) {
+                mma_f16_16816(acc[2 * j + i], ca[0], b[PIECES - 1][2 * i], b[PIECES - 1][2 * i + 1]);
+                mma_f16_16816(acc[2 * j + i], ca[PIECES - 1], b[0][2 * i], b[0][2 * i + 1]);
+              }
+            }
+          }
+        }
+        // M[t][s] = CB exp(cs_t - cs_s) dt_s (+ D where s = t), s <= t
+        const float f = mup / (bup * cup);                  // powers of two
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const int t = r16 + g4 + 4 * j, s = 32 * half + 8 * i + 2 * t4;
+            float v[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float e = exp2_f((hi_s[t] - hi_s[s + u]) + (lo_s[t] - lo_s[s + u])) * dt_s[s + u];
+              v[u] = s + u <= t ? (acc[i][j + u] * f) * e : 0.f;
+              if (s + u == t) v[u] = fmaf(Dh, mup, v[u]);
+            }
+            uint32_t hi, lo;
+            split_h2(v[0], v[1], hi, lo);
+            *reinterpret_cast<uint32_t*>(Ms + t * kSmXS + s) = hi;
+            *reinterpret_cast<uint32_t*>(Ms + (Q + t) * kSmXS + s) = lo;
+          }
+      }
+      // Y2: rows t, columns p = 32 half ..
+      float y2[4][4] = {}, y1[4][4] = {};
+      for (int k = 0; k < NP; k += 16) {
+        uint32_t ca[PIECES][4], b[2][4];
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) ldsm4(ca[u], smem_u32(Cs + u * Q * SN + arow * SN + k + acol));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) ldsm4(b[u], smem_u32(Hs + (u * kSmP + 32 * half + 16 * j + brow) * SN + k + bcol));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma_f16_16816(y2[2 * j + i], ca[0], b[0][2 * i], b[0][2 * i + 1]);
+            mma_f16_16816(y2[2 * j + i], ca[0], b[1][2 * i], b[1][2 * i + 1]);
+            if (PIECES == 2) mma_f16_16816(y2[2 * j + i], ca[PIECES - 1], b[0][2 * i], b[0][2 * i + 1]);
+          }
+        }
+      }
+      __syncthreads();
+      // Y1: only columns s up to the rows' own
+      for (int k = 0; k <= r16; k += 16) {
+        uint32_t ma[2][4], b[PIECES][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) ldsm4(ma[u], smem_u32(Ms + (u * Q + arow) * kSmXS + k + acol));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int u = 0; u < PIECES; ++u)
+            ldsm4t(b[u], smem_u32(Xs + (u * Q + k + krow) * kSmXS + 32 * half + 16 * j + kcol));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma_f16_16816(y1[2 * j + i], ma[0], b[0][2 * i], b[0][2 * i + 1]);
+            mma_f16_16816(y1[2 * j + i], ma[1], b[0][2 * i], b[0][2 * i + 1]);
+            if (PIECES == 2) mma_f16_16816(y1[2 * j + i], ma[0], b[PIECES - 1][2 * i], b[PIECES - 1][2 * i + 1]);
+          }
+        }
+      }
+      const float f1 = 1.f / (mup * xup), f2 = 1.f / (cup * hup);
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const int t = r16 + g4 + 4 * j;
+        const float et = exp2_f(hi_s[t]) * f2;
+        TY* yp = static_cast<TY*>(a.y.p) + (long long)(t0 + t) * a.y.stride + h * P;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = 32 * half + 8 * i + 2 * t4;
+          if (t < n && p < P) {
+            stf(yp + p, fmaf(y2[i][j], et, y1[i][j] * f1));
+            stf(yp + p + 1, fmaf(y2[i][j + 1], et, y1[i][j + 1] * f1));
+          }
+        }
+      }
+    }
+    // S: rows p = r16 .., columns n = half NP / 2 ..
+    float s4[NT][4] = {};
+    for (int k = 0; k < Q; k += 16) {
+      uint32_t wa[2][4], b[PIECES][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) ldsm4t(wa[u], smem_u32(Ws + (u * Q + k + trow) * kSmXS + r16 + tcol));
+      if constexpr (NT == 1) {
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) ldsm4t(b[u], smem_u32(Bs + (u * Q + k + krow) * SN + kcol));      // both halves
+        mma_f16_16816(s4[0], wa[0], b[0][2 * half], b[0][2 * half + 1]);
+        mma_f16_16816(s4[0], wa[1], b[0][2 * half], b[0][2 * half + 1]);
+        if (PIECES == 2) mma_f16_16816(s4[0], wa[0], b[PIECES - 1][2 * half], b[PIECES - 1][2 * half + 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) {
+#pragma unroll
+          for (int u = 0; u < PIECES; ++u)
+            ldsm4t(b[u], smem_u32(Bs + (u * Q + k + krow) * SN + half * (NP / 2) + 16 * j + kcol));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma_f16_16816(s4[2 * j + i], wa[0], b[0][2 * i], b[0][2 * i + 1]);
+            mma_f16_16816(s4[2 * j + i], wa[1], b[0][2 * i], b[0][2 * i + 1]);
+            if (PIECES == 2) mma_f16_16816(s4[2 * j + i], wa[0], b[PIECES - 1][2 * i], b[PIECES - 1][2 * i + 1]);
+          }
+        }
+      }
+    }
+    const float down = 1.f / (wup * bup);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) hs[i][j] = fmaf(hs[i][j], keep, s4[i][j] * down);
+    if (!STATES && t0 + Q < w.t1) put_h();
+    else __syncthreads();          // the tables and tiles have been read
+  }
+  if (STATES || (state && w.k == w.count - 1)) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = r16 + g4 + 8 * (j >> 1), n = half * (NP / 2) + 8 * i + 2 * t4 + (j & 1);
+        if (p < P && n < N) {
+          if (STATES) seg_state[p * N + n] = hs[i][j];
+          else stf(state + p * N + n, hs[i][j]);
+        }
+      }
+  }
+  if (STATES && tid == 0) a.seg_decay[size_t(blockIdx.x) * a.H + h] = exp2_f(float(total_log2));
+}
+
+}  // namespace dfssm

@@ -76,19 +76,6 @@ DFSSM_DEV void umma_f16_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc, 
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
       :: "r"(d), "r"(a), "l"(bd), "r"(idesc), "r"(uint32_t(acc)) : "memory");
 }
-DFSSM_DEV float pow2_f(int k) { return __int_as_float((k + 127) << 23); }       // |k| <= 126
-// k with v 2^k in [2^13, 2^14) (0 for v = 0, and within [-80, 80]).
-DFSSM_DEV int scale_of(float v) {
-  const int e = int((__float_as_uint(v) >> 23) & 0xffu) - 126;                    // v < 2^e
-  return v > 0.f ? max(-80, min(80, 14 - e)) : 0;
-}
-// Two values as fp16 pieces: hi = their fp16 pair, lo that of what is left.
-DFSSM_DEV void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  const float2 f = __half22float2(h);
-  lo = pack_h2(a - f.x, b - f.y);
-}
 DFSSM_DEV void bar_compute() { asm volatile("bar.sync 1, %0;" :: "n"(kStCompute) : "memory"); }
 
 // The two warpgroups of a head.
