@@ -2,6 +2,7 @@
 // host-side checks and launches.  Declarations and semantics: dfssm.h.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 
 #include "dense.cuh"
@@ -152,8 +153,11 @@ bool scan_tc_shape(const dfssm_scan* s, int dtype) {
          s->nheads / s->ngroups % 2 == 0;
 }
 
-// Segments of the prompt form: enough blocks for the SMs, and not much shorter than what
-// the states between segments cost to move.
+// Segments of the prompt form.  A block takes about as long as its chunks and one more (its
+// start, the states in and out); with segments the states before them cost 0.35 of that
+// again for all but each sequence's last, and the join a chunk and a half.  The lengths are on
+// the device: half a chunk is lost at each sequence's end, and the longest is taken for three
+// times the mean.
 struct ScanPlan {
   int seg, max_segs, max_chunks;
   bool split;                                      // more than one segment
@@ -167,11 +171,25 @@ ScanPlan scan_plan(const dfssm_scan* s, ScanPath path, int n_seqs, int n_rows) {
   ScanPlan p;
   const bool tc = path == kScanTc;
   const int unit = tc ? kStQ : path == kScanMma ? kSmQ : kScanQ, heads = tc ? s->nheads / 2 : s->nheads;
-  const long long want = tc ? 2LL * sm_count() : path == kScanMma ? 3LL * sm_count() : 4LL * sm_count();
-  long long seg = ((long long)n_rows * heads + want - 1) / want;
-  seg = std::max<long long>(tc ? 2 * kStQ : 4 * kScanQ, (seg + unit - 1) / unit * unit);
-  p.seg = int(seg);
+  const double slots = double(sm_count()) * (path == kScanSimt ? 2 : 1);
+  const double chunks = double(n_rows) / unit + 0.5 * n_seqs, longest = std::min(double(n_rows), 3.0 * n_rows / std::max(1, n_seqs));
+  auto cost = [&](double most, double blocks) {       // blocks per head, of up to `most` chunks each
+    const double waves = blocks * heads / slots, mean = chunks / blocks + 1;
+    return waves < 4 ? std::ceil(waves) * (std::min(most, 1.5 * (mean - 1)) + 1) : waves * mean + most / 2;
+  };
+  double best = n_seqs > 0 ? cost(longest / unit, n_seqs) : 0;
+  long long seg = n_rows;
+  for (int c : {2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, 24, 32, 48, 64}) {
+    if ((long long)c * unit >= n_rows || n_seqs == 0) break;
+    const double blocks = double(n_rows) / (c * unit) + 0.5 * n_seqs;
+    const double mine = cost(c, blocks) * (1 + 0.35 * std::max(0.0, 1 - n_seqs / blocks)) + 1.5;
+    if (mine < best) {
+      best = mine;
+      seg = (long long)c * unit;
+    }
+  }
   p.split = seg < n_rows;
+  p.seg = int(p.split ? seg : std::max<long long>(unit, (seg + unit - 1) / unit * unit));
   p.max_segs = p.split ? n_rows / p.seg + n_seqs : n_seqs;
   p.max_chunks = tc ? n_rows / kStQ + n_seqs : 0;
   Bump bp;

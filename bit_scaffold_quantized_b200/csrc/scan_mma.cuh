@@ -63,6 +63,22 @@ DFSSM_DEV void store4(__half* hi, int lo_at, const float (&v)[4], float up) {
   if (PIECES == 2) *reinterpret_cast<uint2*>(hi + lo_at) = make_uint2(l[0], l[1]);
 }
 
+// acc[J n tiles] += the products of A's and B's pieces; piece by piece over all tiles, so that
+// no product waits for the one before it.  b[u][j]: piece u of tiles 2 j, 2 j + 1.
+template <int PA, int PB, int J>
+DFSSM_DEV void mma_pieces(float (&acc)[J][4], const uint32_t (&a)[PA][4], const uint32_t (&b)[PB][(J + 1) / 2][4]) {
+#pragma unroll
+  for (int i = 0; i < J; ++i) mma_f16_16816(acc[i], a[0], b[0][i / 2][2 * (i & 1)], b[0][i / 2][2 * (i & 1) + 1]);
+  if (PA == 2) {
+#pragma unroll
+    for (int i = 0; i < J; ++i) mma_f16_16816(acc[i], a[PA - 1], b[0][i / 2][2 * (i & 1)], b[0][i / 2][2 * (i & 1) + 1]);
+  }
+  if (PB == 2) {
+#pragma unroll
+    for (int i = 0; i < J; ++i) mma_f16_16816(acc[i], a[0], b[PB - 1][i / 2][2 * (i & 1)], b[PB - 1][i / 2][2 * (i & 1) + 1]);
+  }
+}
+
 template <typename TX, typename TY, typename TS, int NP, bool STATES>
 __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
   pdl_wait();
@@ -235,22 +251,14 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
       float acc[4][4] = {};
       if (32 * half <= r16 + 15) {
         for (int k = 0; k < NP; k += 16) {
-          uint32_t ca[PIECES][4], b[PIECES][4];
+          uint32_t ca[PIECES][4], b[PIECES][2][4];
 #pragma unroll
-          for (int u = 0; u < PIECES; ++u) ldsm4(ca[u], smem_u32(Cs + u * Q * SN + arow * SN + k + acol));
+          for (int u = 0; u < PIECES; ++u) {
+            ldsm4(ca[u], smem_u32(Cs + u * Q * SN + arow * SN + k + acol));
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int u = 0; u < PIECES; ++u) ldsm4(b[u], smem_u32(Bs + u * Q * SN + (32 * half + 16 * j + brow) * SN + k + bcol));
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              mma_f16_16816(acc[2 * j + i], ca[0], b[0][2 * i], b[0][2 * i + 1]);
-              if (PIECES == 2) {
-                mma_f16_16816(acc[2 * j + i], ca[0], b[PIECES - 1][2 * i], b[PIECES - 1][2 * i + 1]);
-                mma_f16_16816(acc[2 * j + i], ca[PIECES - 1], b[0][2 * i], b[0][2 * i + 1]);
-              }
-            }
+            for (int j = 0; j < 2; ++j) ldsm4(b[u][j], smem_u32(Bs + u * Q * SN + (32 * half + 16 * j + brow) * SN + k + bcol));
           }
+          mma_pieces<PIECES, PIECES, 4>(acc, ca, b);
         }
         // M[t][s] = CB exp(cs_t - cs_s) dt_s (+ D where s = t), s <= t
         const float f = mup / (bup * cup);                  // powers of two
@@ -275,39 +283,27 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
       // Y2: rows t, columns p = 32 half ..
       float y2[4][4] = {}, y1[4][4] = {};
       for (int k = 0; k < NP; k += 16) {
-        uint32_t ca[PIECES][4], b[2][4];
+        uint32_t ca[PIECES][4], b[2][2][4];
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) ldsm4(ca[u], smem_u32(Cs + u * Q * SN + arow * SN + k + acol));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) ldsm4(b[u], smem_u32(Hs + (u * kSmP + 32 * half + 16 * j + brow) * SN + k + bcol));
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mma_f16_16816(y2[2 * j + i], ca[0], b[0][2 * i], b[0][2 * i + 1]);
-            mma_f16_16816(y2[2 * j + i], ca[0], b[1][2 * i], b[1][2 * i + 1]);
-            if (PIECES == 2) mma_f16_16816(y2[2 * j + i], ca[PIECES - 1], b[0][2 * i], b[0][2 * i + 1]);
-          }
-        }
+          for (int j = 0; j < 2; ++j) ldsm4(b[u][j], smem_u32(Hs + (u * kSmP + 32 * half + 16 * j + brow) * SN + k + bcol));
+        mma_pieces<PIECES, 2, 4>(y2, ca, b);
       }
       __syncthreads();
       // Y1: only columns s up to the rows' own
       for (int k = 0; k <= r16; k += 16) {
-        uint32_t ma[2][4], b[PIECES][4];
+        uint32_t ma[2][4], b[PIECES][2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) ldsm4(ma[u], smem_u32(Ms + (u * Q + arow) * kSmXS + k + acol));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int u = 0; u < PIECES; ++u)
 #pragma unroll
-          for (int u = 0; u < PIECES; ++u)
-            ldsm4t(b[u], smem_u32(Xs + (u * Q + k + krow) * kSmXS + 32 * half + 16 * j + kcol));
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mma_f16_16816(y1[2 * j + i], ma[0], b[0][2 * i], b[0][2 * i + 1]);
-            mma_f16_16816(y1[2 * j + i], ma[1], b[0][2 * i], b[0][2 * i + 1]);
-            if (PIECES == 2) mma_f16_16816(y1[2 * j + i], ma[0], b[PIECES - 1][2 * i], b[PIECES - 1][2 * i + 1]);
-          }
-        }
+          for (int j = 0; j < 2; ++j)
+            ldsm4t(b[u][j], smem_u32(Xs + (u * Q + k + krow) * kSmXS + 32 * half + 16 * j + kcol));
+        mma_pieces<2, PIECES, 4>(y1, ma, b);
       }
       const float f1 = 1.f / (mup * xup), f2 = 1.f / (cup * hup);
 #pragma unroll
@@ -328,29 +324,21 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
     // S: rows p = r16 .., columns n = half NP / 2 ..
     float s4[NT][4] = {};
     for (int k = 0; k < Q; k += 16) {
-      uint32_t wa[2][4], b[PIECES][4];
+      constexpr int J = (NT + 1) / 2;
+      uint32_t wa[2][4], b[PIECES][J][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) ldsm4t(wa[u], smem_u32(Ws + (u * Q + k + trow) * kSmXS + r16 + tcol));
-      if constexpr (NT == 1) {
 #pragma unroll
-        for (int u = 0; u < PIECES; ++u) ldsm4t(b[u], smem_u32(Bs + (u * Q + k + krow) * SN + kcol));      // both halves
-        mma_f16_16816(s4[0], wa[0], b[0][2 * half], b[0][2 * half + 1]);
-        mma_f16_16816(s4[0], wa[1], b[0][2 * half], b[0][2 * half + 1]);
-        if (PIECES == 2) mma_f16_16816(s4[0], wa[0], b[PIECES - 1][2 * half], b[PIECES - 1][2 * half + 1]);
-      } else {
+      for (int u = 0; u < PIECES; ++u) {
 #pragma unroll
-        for (int j = 0; j < NT / 2; ++j) {
-#pragma unroll
-          for (int u = 0; u < PIECES; ++u)
-            ldsm4t(b[u], smem_u32(Bs + (u * Q + k + krow) * SN + half * (NP / 2) + 16 * j + kcol));
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mma_f16_16816(s4[2 * j + i], wa[0], b[0][2 * i], b[0][2 * i + 1]);
-            mma_f16_16816(s4[2 * j + i], wa[1], b[0][2 * i], b[0][2 * i + 1]);
-            if (PIECES == 2) mma_f16_16816(s4[2 * j + i], wa[0], b[PIECES - 1][2 * i], b[PIECES - 1][2 * i + 1]);
-          }
+        for (int j = 0; j < J; ++j)
+          ldsm4t(b[u][j], smem_u32(Bs + (u * Q + k + krow) * SN + (NT == 1 ? 0 : half * (NP / 2) + 16 * j) + kcol));
+        if (NT == 1 && half == 1) {           // both halves' eight columns came: take the second
+          b[u][0][0] = b[u][0][2];
+          b[u][0][1] = b[u][0][3];
         }
       }
+      mma_pieces<2, PIECES, NT>(s4, wa, b);
     }
     const float down = 1.f / (wup * bup);
 #pragma unroll
