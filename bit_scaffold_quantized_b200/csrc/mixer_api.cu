@@ -303,7 +303,7 @@ int scan_mma_launch(const ScanArgs& a, cudaStream_t st) {
 
 template <typename TX, typename TY, typename TS>
 int scan_mma_shape(const ScanArgs& a, cudaStream_t st) {
-  if (a.N <= 16) return scan_mma_launch<TX, TY, TS, 16>(a, st);
+  if (a.N <= 32) return scan_mma_launch<TX, TY, TS, 32>(a, st);
   if (a.N <= 64) return scan_mma_launch<TX, TY, TS, 64>(a, st);
   return scan_mma_launch<TX, TY, TS, 128>(a, st);
 }

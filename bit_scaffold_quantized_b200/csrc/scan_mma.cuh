@@ -12,11 +12,14 @@ namespace dfssm {
 //   fp32 values go in as two fp16 pieces, value = hi + lo to 2^-22, scaled by a power of two
 //   (x, B and C by the chunk's largest, M, W and H by bounds) so that the largest lies below
 //   2^14, and three products hi hi + hi lo + lo hi; fp16 rows are exact in one piece.
-// 8 warps.  CB, Y1, Y2: warp = 16 rows t x half of the columns; S and H: warp = 16 rows p x
-// half of the columns n, H in registers (fp32) throughout.  The next chunk's rows are on
+// 16 warps (eight of twice the work had too little to do while they waited).  CB, Y1, Y2: warp =
+// 16 rows t x a quarter of the columns; S and H: warp = 16 rows p x a quarter of the columns n,
+// H in registers (fp32) throughout.  The next chunk's rows are on
 // their way in registers meanwhile.
-// The legacy tensor path suffices: 1000 rows of the 64-head layer in fp32 take MMA_FIGURES.
-constexpr int kSmQ = 64, kSmP = 64, kSmThreads = 256;
+// The legacy tensor path suffices: 1000 rows of the 64-head layer in fp32 take 125 us with
+// the states between segments (93 for this kernel); its bound is the shared memory: an operand
+// fragment is read again by each of the four warps that need it.
+constexpr int kSmQ = 64, kSmP = 64, kSmThreads = 512;
 constexpr int kSmXS = kSmP + 8;          // row strides in halves: 16 bytes past a multiple of 128, so that
                                           // ldmatrix's eight rows lie in different banks
 __host__ __device__ constexpr int sm_ns(int np) { return np + 8; }
@@ -84,7 +87,7 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
   pdl_wait();
   pdl_release();
   constexpr int PIECES = sizeof(TX) == 4 ? 2 : 1, SN = sm_ns(NP), Q = kSmQ;
-  constexpr int NT = NP / 16;                           // n tiles of a warp's half of the state
+  constexpr int NT = NP / 32;                           // n tiles of a warp's quarter of the state
   constexpr int GX = Q * kSmP / 4 / kSmThreads, GN = Q * NP / 4 / kSmThreads;      // groups of four per thread
   extern __shared__ __align__(16) unsigned char sm_raw[];
   __half* const Bs = reinterpret_cast<__half*>(sm_raw);             // [PIECES][Q][SN]
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
   __half* const Ms = Ws + 2 * Q * kSmXS;                            // [2][Q][kSmXS]
   __half* const Cs = Ms + 2 * Q * kSmXS;                            // [PIECES][Q][SN]
   __half* const Hs = Cs + PIECES * Q * SN;                          // [2][kSmP][SN]
-  __shared__ float hi_s[Q], lo_s[Q], dt_s[Q], w_s[Q], red[4][8], sums[3];      // sums: exp(cs_Q), max dt, max w
+  __shared__ __align__(16) float hi_s[Q], lo_s[Q], dt_s[Q], w_s[Q], red[4][16], sums[3];      // sums: exp(cs_Q), max dt, max w
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, t4 = lane & 3;
   const int P = a.P, N = a.N, h = blockIdx.y, g = h / (a.H / a.G);
   SegWork w;
@@ -107,17 +110,17 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
   TS* const state = a.state ? static_cast<TS*>(a.state) + (size_t(slot) * a.H + h) * P * N : nullptr;
   float* const seg_state = a.seg_state + (size_t(blockIdx.x) * a.H + h) * P * N;
   const bool old = !STATES && w.count == 1 && state && !(a.q.fresh && a.q.fresh[w.s]);
-  const int r16 = 16 * (warp & 3), half = warp >> 2;    // the warp's rows (t or p), its half of the columns
+  const int r16 = 16 * (warp & 3), part = warp >> 2;    // the warp's rows (t or p), its quarter of the columns
   const double rate = -exp(double(a.A_log[h])), log2e = 1.4426950408889634;
   const float bias = a.dt_bias[h], Dh = a.D ? a.D[h] : 0.f;
 
-  // H: rows r16 + g4 (+ 8), columns half NP / 2 + 8 i + 2 t4 (+ 1)
+  // H: rows r16 + g4 (+ 8), columns part NP / 4 + 8 i + 2 t4 (+ 1)
   float hs[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int p = r16 + g4 + 8 * (j >> 1), n = half * (NP / 2) + 8 * i + 2 * t4 + (j & 1);
+      const int p = r16 + g4 + 8 * (j >> 1), n = part * (NP / 4) + 8 * i + 2 * t4 + (j & 1);
       hs[i][j] = 0.f;
       if (!STATES && p < P && n < N) {
         if (w.count > 1) hs[i][j] = seg_state[p * N + n];
@@ -130,8 +133,13 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
     if (lane == 0) red[which][warp] = m;
   };
   auto red_top = [&](int which) {
-    const float4 u = *reinterpret_cast<const float4*>(&red[which][0]), v = *reinterpret_cast<const float4*>(&red[which][4]);
-    return fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSmThreads / 32; i += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(&red[which][i]);
+      m = fmaxf(m, fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)));
+    }
+    return m;
   };
   auto put_h = [&]() {
     float m = 0.f;
@@ -146,7 +154,7 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
       for (int j = 0; j < 4; j += 2) {
         uint32_t hi, lo;
         split_h2(hs[i][j] * hup, hs[i][j + 1] * hup, hi, lo);
-        __half* at = Hs + (r16 + g4 + 4 * j) * SN + half * (NP / 2) + 8 * i + 2 * t4;
+        __half* at = Hs + (r16 + g4 + 4 * j) * SN + part * (NP / 4) + 8 * i + 2 * t4;
         *reinterpret_cast<uint32_t*>(at) = hi;
         *reinterpret_cast<uint32_t*>(at + kSmP * SN) = lo;
       }
@@ -247,26 +255,25 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
     const int brow = (lane & 7) + 8 * (lane >> 4), bcol = 8 * ((lane >> 3) & 1);   // B as it lies: rows n
     const int krow = lane & 15, kcol = 8 * (lane >> 4);                       // B transposed: rows k
     if (!STATES) {
-      // CB: rows t = r16 .., columns s = 32 half ..
-      float acc[4][4] = {};
-      if (32 * half <= r16 + 15) {
+      // CB: rows t = r16 .., columns s = 16 part ..
+      float acc[2][4] = {};
+      if (16 * part <= r16) {
         for (int k = 0; k < NP; k += 16) {
-          uint32_t ca[PIECES][4], b[PIECES][2][4];
+          uint32_t ca[PIECES][4], b[PIECES][1][4];
 #pragma unroll
           for (int u = 0; u < PIECES; ++u) {
             ldsm4(ca[u], smem_u32(Cs + u * Q * SN + arow * SN + k + acol));
-#pragma unroll
-            for (int j = 0; j < 2; ++j) ldsm4(b[u][j], smem_u32(Bs + u * Q * SN + (32 * half + 16 * j + brow) * SN + k + bcol));
+            ldsm4(b[u][0], smem_u32(Bs + u * Q * SN + (16 * part + brow) * SN + k + bcol));
           }
-          mma_pieces<PIECES, PIECES, 4>(acc, ca, b);
+          mma_pieces<PIECES, PIECES, 2>(acc, ca, b);
         }
         // M[t][s] = CB exp(cs_t - cs_s) dt_s (+ D where s = t), s <= t
         const float f = mup / (bup * cup);                  // powers of two
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int j = 0; j < 4; j += 2) {
-            const int t = r16 + g4 + 4 * j, s = 32 * half + 8 * i + 2 * t4;
+            const int t = r16 + g4 + 4 * j, s = 16 * part + 8 * i + 2 * t4;
             float v[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -280,30 +287,25 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
             *reinterpret_cast<uint32_t*>(Ms + (Q + t) * kSmXS + s) = lo;
           }
       }
-      // Y2: rows t, columns p = 32 half ..
-      float y2[4][4] = {}, y1[4][4] = {};
+      // Y2: rows t, columns p = 16 part ..
+      float y2[2][4] = {}, y1[2][4] = {};
       for (int k = 0; k < NP; k += 16) {
-        uint32_t ca[PIECES][4], b[2][2][4];
+        uint32_t ca[PIECES][4], b[2][1][4];
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) ldsm4(ca[u], smem_u32(Cs + u * Q * SN + arow * SN + k + acol));
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) ldsm4(b[u][j], smem_u32(Hs + (u * kSmP + 32 * half + 16 * j + brow) * SN + k + bcol));
-        mma_pieces<PIECES, 2, 4>(y2, ca, b);
+        for (int u = 0; u < 2; ++u) ldsm4(b[u][0], smem_u32(Hs + (u * kSmP + 16 * part + brow) * SN + k + bcol));
+        mma_pieces<PIECES, 2, 2>(y2, ca, b);
       }
       __syncthreads();
       // Y1: only columns s up to the rows' own
       for (int k = 0; k <= r16; k += 16) {
-        uint32_t ma[2][4], b[PIECES][2][4];
+        uint32_t ma[2][4], b[PIECES][1][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) ldsm4(ma[u], smem_u32(Ms + (u * Q + arow) * kSmXS + k + acol));
 #pragma unroll
-        for (int u = 0; u < PIECES; ++u)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            ldsm4t(b[u][j], smem_u32(Xs + (u * Q + k + krow) * kSmXS + 32 * half + 16 * j + kcol));
-        mma_pieces<2, PIECES, 4>(y1, ma, b);
+        for (int u = 0; u < PIECES; ++u) ldsm4t(b[u][0], smem_u32(Xs + (u * Q + k + krow) * kSmXS + 16 * part + kcol));
+        mma_pieces<2, PIECES, 2>(y1, ma, b);
       }
       const float f1 = 1.f / (mup * xup), f2 = 1.f / (cup * hup);
 #pragma unroll
@@ -312,8 +314,8 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
         const float et = exp2_f(hi_s[t]) * f2;
         TY* yp = static_cast<TY*>(a.y.p) + (long long)(t0 + t) * a.y.stride + h * P;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int p = 32 * half + 8 * i + 2 * t4;
+        for (int i = 0; i < 2; ++i) {
+          const int p = 16 * part + 8 * i + 2 * t4;
           if (t < n && p < P) {
             stf(yp + p, fmaf(y2[i][j], et, y1[i][j] * f1));
             stf(yp + p + 1, fmaf(y2[i][j + 1], et, y1[i][j + 1] * f1));
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
         }
       }
     }
-    // S: rows p = r16 .., columns n = half NP / 2 ..
+    // S: rows p = r16 .., columns n = part NP / 4 ..
     float s4[NT][4] = {};
     for (int k = 0; k < Q; k += 16) {
       constexpr int J = (NT + 1) / 2;
@@ -332,8 +334,8 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
       for (int u = 0; u < PIECES; ++u) {
 #pragma unroll
         for (int j = 0; j < J; ++j)
-          ldsm4t(b[u][j], smem_u32(Bs + (u * Q + k + krow) * SN + (NT == 1 ? 0 : half * (NP / 2) + 16 * j) + kcol));
-        if (NT == 1 && half == 1) {           // both halves' eight columns came: take the second
+          ldsm4t(b[u][j], smem_u32(Bs + (u * Q + k + krow) * SN + (NT == 1 ? 16 * (part >> 1) : part * (NP / 4) + 16 * j) + kcol));
+        if (NT == 1 && (part & 1)) {          // two warps' eight columns came: take the second
           b[u][0][0] = b[u][0][2];
           b[u][0][1] = b[u][0][3];
         }
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int p = r16 + g4 + 8 * (j >> 1), n = half * (NP / 2) + 8 * i + 2 * t4 + (j & 1);
+        const int p = r16 + g4 + 8 * (j >> 1), n = part * (NP / 4) + 8 * i + 2 * t4 + (j & 1);
         if (p < P && n < N) {
           if (STATES) seg_state[p * N + n] = hs[i][j];
           else stf(state + p * N + n, hs[i][j]);
