@@ -6,6 +6,10 @@ nvcc cross-compiles without a GPU.  The library links the CUDA runtime staticall
 and exports only the C ABI declared in include/dfssm.h.  The "phases" variant
 (libdfssm_phases.so) is the same library with the batch-1 token kernel's per-phase
 cycle counters compiled in (-DDFSSM_PHASE_TIMERS), for bit_scaffold_quantized_b200.phases.
+
+Beside the library, g++ builds _binding.so (csrc/binding.cpp): the checks and the marshalling
+of PyTorch tensors for the calls that take a few microseconds, against the installed
+PyTorch's headers.
 """
 from __future__ import annotations
 
@@ -31,8 +35,27 @@ FLAGS = [
 ]
 
 
+BINDING = os.path.join(PKG, "_binding.so")
+CXX = os.environ.get("CXX", "g++")
+
+
+def _binding_cmd(out: str):
+    """The command that builds csrc/binding.cpp as the extension module _binding."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w", "-DTORCH_EXTENSION_NAME=_binding",
+            f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *[a for d in inc for a in ("-isystem", d)], os.path.join(CSRC, "binding.cpp"),
+            "-o", out, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".cpp"))]
     files.append(os.path.join(INCLUDE, "dfssm.h"))
     files.append(os.path.abspath(__file__))
     return files
@@ -47,13 +70,14 @@ def up_to_date(lib: str = LIB) -> bool:
 
 def build(force: bool = False, verbose: bool = False, variant: str = "") -> str:
     defines, lib = VARIANTS[variant]
-    if not force and up_to_date(lib):
+    if not force and up_to_date(lib) and up_to_date(BINDING):
         return lib
     with tempfile.TemporaryDirectory(prefix="dfssm_build_") as tmp:
         objs = [os.path.join(tmp, src + ".o") for src in SOURCES]
         cmds = [[NVCC, *(["-Xptxas=-v"] if verbose else []), *FLAGS, *defines, "-I", INCLUDE, "-I", CSRC, "-c",
                  os.path.join(CSRC, src), "-o", obj] for src, obj in zip(SOURCES, objs)]
         procs = []
+        cmds.append(_binding_cmd(BINDING + ".tmp"))
         for cmd in cmds:                      # the sources compile side by side
             if verbose:
                 print(" ".join(cmd))
@@ -63,6 +87,7 @@ def build(force: bool = False, verbose: bool = False, variant: str = "") -> str:
                 raise subprocess.CalledProcessError(code, cmd)
         subprocess.run([NVCC, *FLAGS, "-shared", "-o", lib + ".tmp", *objs], check=True)
     os.replace(lib + ".tmp", lib)
+    os.replace(BINDING + ".tmp", BINDING)
     return lib
 
 

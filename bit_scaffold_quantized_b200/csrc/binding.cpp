@@ -1,0 +1,203 @@
+// Argument marshalling of the parts of a layer (conv, scan, gated norm, dense projection)
+// from PyTorch tensors to the C ABI: shapes, types and devices are checked here and the
+// small structs filled.  A single token's call takes a few microseconds on the GPU; the same
+// checks in Python took twice that.  The functions are reached by the addresses that the
+// Python side takes from the loaded libdfssm.so.
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/extension.h>
+
+#include <optional>
+#include <stdexcept>
+#include <string>
+
+#include "dfssm.h"
+
+namespace {
+
+using at::Tensor;
+using Opt = std::optional<Tensor>;
+using Addr = uintptr_t;
+
+[[noreturn]] void bad(const std::string& what) { throw std::invalid_argument(what); }
+
+std::string describe(const Tensor& t) {
+  std::string s = std::string(c10::toString(t.scalar_type())) + " [";
+  for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.size(i));
+  s += "] with strides [";
+  for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.stride(i));
+  return s + "]";
+}
+
+// All tensors of a call lie on one CUDA device: the first one's.
+struct Device {
+  int index = -1;
+  void take(const Tensor& t, const char* name) {
+    if (!t.is_cuda()) bad(std::string(name) + " does not lie on a CUDA device");
+    if (index < 0) index = t.get_device();
+    else if (index != t.get_device()) bad(std::string("all tensors must lie on one CUDA device: ") + name + " does not");
+  }
+};
+
+int type_of(const Tensor& t, const char* name) {
+  if (t.scalar_type() == at::kHalf) return DFSSM_DTYPE_F16;
+  if (t.scalar_type() == at::kFloat) return DFSSM_DTYPE_F32;
+  bad(std::string(name) + " must be float16 or float32, not " + describe(t));
+}
+
+dfssm_rows rows(Device& d, const Tensor& t, const char* name, int64_t n, int64_t width) {
+  if (t.dim() != 2 || t.size(0) != n || t.size(1) != width || (width > 1 && t.stride(1) != 1))
+    bad(std::string(name) + " must be [" + std::to_string(n) + ", " + std::to_string(width) +
+        "] with contiguous rows, not " + describe(t));
+  dfssm_rows r;
+  r.dtype = type_of(t, name);
+  d.take(t, name);
+  r.data = t.data_ptr();
+  r.stride = n > 1 ? t.stride(0) : std::max(t.stride(0), width);
+  return r;
+}
+
+void* array(Device& d, const Opt& t, const char* name, at::ScalarType type, at::IntArrayRef shape) {
+  if (!t) return nullptr;
+  if (t->scalar_type() != type || t->sizes() != shape || !t->is_contiguous()) {
+    std::string s;
+    for (int64_t v : shape) s += (s.empty() ? "" : ", ") + std::to_string(v);
+    bad(std::string(name) + " must be a contiguous " + c10::toString(type) + " tensor [" + s + "], not " + describe(*t));
+  }
+  d.take(*t, name);
+  return t->data_ptr();
+}
+
+int size32(int64_t v, const char* name) {
+  if (v < 0 || v > INT32_MAX) bad(std::string(name) + " is out of range");
+  return int(v);
+}
+
+dfssm_seqs seqs(Device& d, int64_t n_rows, const Opt& start, const Opt& slot, const Opt& fresh, const Opt& status,
+                int64_t slots) {
+  if (start && (start->dim() != 1 || start->size(0) < 1)) bad("start must hold one more entry than there are sequences");
+  const int64_t n = start ? start->size(0) - 1 : n_rows;
+  dfssm_seqs q;
+  q.n_seqs = size32(n, "the number of sequences");
+  q.n_rows = size32(n_rows, "the number of rows");
+  q.n_slots = size32(slots, "the number of slots");
+  q.start = static_cast<const int32_t*>(array(d, start, "start", at::kInt, {n + 1}));
+  q.slot = static_cast<const int32_t*>(array(d, slot, "slot", at::kInt, {n}));
+  q.fresh = static_cast<const int32_t*>(array(d, fresh, "fresh", at::kInt, {n}));
+  q.status = static_cast<uint32_t*>(array(d, status, "status", at::kInt, {1}));
+  return q;
+}
+
+// f(stream) on the tensors' device, on that device's current stream unless one is given.
+template <typename F>
+int on_device(const Device& d, const std::optional<Addr>& stream, F f) {
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(d.index));
+  return f(stream ? reinterpret_cast<void*>(*stream)
+                  : static_cast<void*>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(d.index)).stream()));
+}
+
+int conv(Addr fn, const Tensor& x, const Tensor& w, const Opt& b, const Opt& state, const Tensor& y, const Opt& start,
+         const Opt& slot, const Opt& fresh, bool silu, const Opt& status, const std::optional<Addr>& stream) {
+  if (x.dim() != 2 || w.dim() != 2) bad("x and w must be matrices");
+  Device d;
+  const int64_t n = x.size(0), c = x.size(1), width = w.size(1), slots = state ? state->size(0) : 0;
+  const dfssm_rows xr = rows(d, x, "x", n, c), yr = rows(d, y, "y", n, c);
+  const auto* wp = static_cast<const uint16_t*>(array(d, w, "w", at::kHalf, {c, width}));
+  const auto* bp = static_cast<const uint16_t*>(array(d, b, "b", at::kHalf, {c}));
+  auto* sp = static_cast<float*>(array(d, state, "state", at::kFloat, {slots, width - 1, c}));
+  const dfssm_seqs q = seqs(d, n, start, slot, fresh, status, slots);
+  const int channels = size32(c, "channels"), taps = size32(width, "d_conv");
+  return on_device(d, stream, [&](void* st) {
+    return reinterpret_cast<decltype(&dfssm_conv_token)>(fn)(channels, taps, silu, &xr, wp, bp, &q, sp, &yr, st);
+  });
+}
+
+int scan(Addr fn, const Tensor& x, const Tensor& dt, const Tensor& B, const Tensor& C, const Tensor& dt_bias,
+         const Tensor& A_log, const Opt& D, const Opt& state, const Tensor& y, const Opt& start, const Opt& ws,
+         const Opt& slot, const Opt& fresh, const Opt& status, std::optional<int64_t> headdim,
+         std::optional<int64_t> groups, const std::optional<Addr>& stream) {
+  if (x.dim() != 2 || B.dim() != 2 || dt_bias.dim() != 1) bad("x and B must be matrices, dt_bias a vector");
+  Device d;
+  const int64_t n = x.size(0), H = dt_bias.size(0);
+  int64_t P, N, G, slots = 0;
+  dfssm_scan s{};
+  s.state_dtype = DFSSM_DTYPE_F32;
+  if (state) {
+    if (state->dim() != 4 || state->size(1) != H || !state->is_contiguous())
+      bad("state must be contiguous [slots, heads, headdim, d_state], not " + describe(*state));
+    s.state_dtype = type_of(*state, "state");
+    d.take(*state, "state");
+    slots = state->size(0);
+    P = state->size(2);
+    N = state->size(3);
+    G = N ? B.size(1) / N : 0;
+  } else {
+    if (!headdim || !groups || *groups < 1) bad("without a state, headdim and groups must be given");
+    P = *headdim;
+    G = *groups;
+    N = B.size(1) / G;
+  }
+  s.nheads = size32(H, "the number of heads");
+  s.headdim = size32(P, "headdim");
+  s.d_state = size32(N, "d_state");
+  s.ngroups = size32(G, "groups");
+  s.dt_bias = static_cast<const float*>(array(d, dt_bias, "dt_bias", at::kFloat, {H}));
+  s.A_log = static_cast<const float*>(array(d, A_log, "A_log", at::kFloat, {H}));
+  s.D = static_cast<const float*>(array(d, D, "D", at::kFloat, {H}));
+  const dfssm_rows xr = rows(d, x, "x", n, H * P), dr = rows(d, dt, "dt", n, H), br = rows(d, B, "B", n, G * N),
+                   cr = rows(d, C, "C", n, G * N), yr = rows(d, y, "y", n, H * P);
+  const dfssm_seqs q = seqs(d, n, start, slot, fresh, status, slots);
+  void* sp = state ? state->data_ptr() : nullptr;
+  if (!start)
+    return on_device(d, stream, [&](void* st) {
+      return reinterpret_cast<decltype(&dfssm_scan_token)>(fn)(&s, &xr, &dr, &br, &cr, &q, sp, &yr, st);
+    });
+  if (!ws || !ws->is_contiguous()) bad("ws must be a contiguous tensor (scan_workspace)");
+  d.take(*ws, "ws");
+  return on_device(d, stream, [&](void* st) {
+    return reinterpret_cast<decltype(&dfssm_scan_prompt)>(fn)(&s, &xr, &dr, &br, &cr, &q, sp, &yr, ws->data_ptr(),
+                                                              size_t(ws->nbytes()), st);
+  });
+}
+
+int gated_norm(Addr fn, const Tensor& y, const Opt& z, const Tensor& w, const Tensor& out, int64_t groups,
+               const std::optional<Addr>& stream) {
+  if (y.dim() != 2) bad("y must be a matrix");
+  Device d;
+  const int64_t n = y.size(0), c = y.size(1);
+  const dfssm_rows yr = rows(d, y, "y", n, c), outr = rows(d, out, "out", n, c);
+  dfssm_rows zr{};
+  if (z) zr = rows(d, *z, "z", n, c);
+  const auto* wp = static_cast<const uint16_t*>(array(d, w, "w", at::kHalf, {c}));
+  const int rn = size32(n, "rows"), cn = size32(c, "cols"), gn = size32(groups, "groups");
+  return on_device(d, stream, [&](void* st) {
+    return reinterpret_cast<decltype(&dfssm_gated_norm)>(fn)(rn, cn, gn, &yr, z ? &zr : nullptr, wp, &outr, st);
+  });
+}
+
+int dense_forward(Addr fn, const Tensor& w, const Tensor& x, const Tensor& y, const Opt& bias, const Opt& residual,
+                  bool silu, const Opt& status, const std::optional<Addr>& stream) {
+  if (w.dim() != 2 || x.dim() != 2) bad("w and x must be matrices");
+  Device d;
+  const int64_t r = w.size(0), c = w.size(1), n = x.size(0);
+  const dfssm_rows xr = rows(d, x, "x", n, c), yr = rows(d, y, "y", n, r);
+  dfssm_rows rr{};
+  if (residual) rr = rows(d, *residual, "residual", n, r);
+  const auto* wp = static_cast<const uint16_t*>(array(d, w, "w", at::kHalf, {r, c}));
+  const auto* bp = static_cast<const uint16_t*>(array(d, bias, "bias", at::kHalf, {r}));
+  auto* sp = static_cast<uint32_t*>(array(d, status, "status", at::kInt, {1}));
+  const int rn = size32(r, "rows"), cn = size32(c, "cols"), bn = size32(n, "batch");
+  return on_device(d, stream, [&](void* st) {
+    return reinterpret_cast<decltype(&dfssm_dense_forward)>(fn)(rn, cn, bn, wp, bp, silu, &xr, residual ? &rr : nullptr,
+                                                                &yr, sp, st);
+  });
+}
+
+}  // namespace
+
+PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
+  m.def("conv", &conv);
+  m.def("scan", &scan);
+  m.def("gated_norm", &gated_norm);
+  m.def("dense_forward", &dense_forward);
+}

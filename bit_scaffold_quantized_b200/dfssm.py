@@ -9,9 +9,8 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-import struct as _struct
 from dataclasses import dataclass
-from typing import List, Optional, Sequence, Tuple
+from typing import List, Optional, Sequence
 
 import numpy as np
 
@@ -82,6 +81,20 @@ class CWsLayout(C.Structure):
                  "res", "scratch", "control")]
 
 
+class CRows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("stride", C.c_int64), ("dtype", C.c_int32)]
+
+
+class CSeqs(C.Structure):
+    _fields_ = [("n_seqs", C.c_int32), ("n_rows", C.c_int32), ("n_slots", C.c_int32), ("start", C.c_void_p),
+                ("slot", C.c_void_p), ("fresh", C.c_void_p), ("status", C.c_void_p)]
+
+
+class CScan(C.Structure):
+    _fields_ = [("nheads", C.c_int32), ("headdim", C.c_int32), ("d_state", C.c_int32), ("ngroups", C.c_int32),
+                ("state_dtype", C.c_int32), ("dt_bias", C.c_void_p), ("A_log", C.c_void_p), ("D", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -126,14 +139,14 @@ def lib() -> C.CDLL:
     L.dfssm_df_field_words.argtypes = [i]
     L.dfssm_df_encode.argtypes = [vp, i, i, vp, vp, vp, vp, vp]
     L.dfssm_df_decode.argtypes = [vp, vp, vp, i, i, vp, vp]
-    st = C.c_char_p                      # a packed struct (the parts of a layer, below)
-    L.dfssm_conv_prompt.argtypes = L.dfssm_conv_token.argtypes = [i, i, i, st, vp, vp, st, vp, st, vp]
-    L.dfssm_scan_workspace_bytes.argtypes = [st, i, i, i]
+    rows, seqs, scan = C.POINTER(CRows), C.POINTER(CSeqs), C.POINTER(CScan)
+    L.dfssm_conv_prompt.argtypes = L.dfssm_conv_token.argtypes = [i, i, i, rows, vp, vp, seqs, vp, rows, vp]
+    L.dfssm_scan_workspace_bytes.argtypes = [scan, i, i, i]
     L.dfssm_scan_workspace_bytes.restype = sz
-    L.dfssm_scan_prompt.argtypes = [st, st, st, st, st, st, vp, st, vp, sz, vp]
-    L.dfssm_scan_token.argtypes = [st, st, st, st, st, st, vp, st, vp]
-    L.dfssm_gated_norm.argtypes = [i, i, i, st, st, vp, st, vp]
-    L.dfssm_dense_forward.argtypes = [i, i, i, vp, vp, i, st, st, st, vp, vp]
+    L.dfssm_scan_prompt.argtypes = [scan, rows, rows, rows, rows, seqs, vp, rows, vp, sz, vp]
+    L.dfssm_scan_token.argtypes = [scan, rows, rows, rows, rows, seqs, vp, rows, vp]
+    L.dfssm_gated_norm.argtypes = [i, i, i, rows, rows, vp, rows, vp]
+    L.dfssm_dense_forward.argtypes = [i, i, i, vp, vp, i, rows, rows, rows, vp, vp]
     L.dfssm_last_error.restype = C.c_char_p
     L.dfssm_version.restype = C.c_int
     for name in EXPORTS:
@@ -446,74 +459,34 @@ def df_decode(cells, lo, span, rows, stream=None) -> None:
 
 # ------------------------------------------------------------------ the parts of a layer
 
-# Their small structs (dfssm_rows, dfssm_seqs, dfssm_scan) are packed in one go: a token's
-# calls take microseconds, and filling ctypes fields one by one would be most of that.
-_ROWS = _struct.Struct("@Pqi4x").pack
-_SEQS = _struct.Struct("@iii4xPPPP").pack
-_SCAN = _struct.Struct("@iiiii4xPPP").pack
-_TYPES: dict = {}
+# Their checks and marshalling are compiled (csrc/binding.cpp): a token's calls take
+# microseconds, and doing it here would be most of that.  It is handed the addresses of the
+# library's functions, so that it calls whichever library lib() has loaded.
+_PARTS = ("dfssm_conv_prompt", "dfssm_conv_token", "dfssm_scan_prompt", "dfssm_scan_token", "dfssm_gated_norm",
+          "dfssm_dense_forward")
+_parts = None
 
 
-def _init_types() -> dict:
-    import torch
-    _TYPES.update({torch.float16: DTYPE_F16, torch.float32: DTYPE_F32, "f16": torch.float16, "f32": torch.float32,
-                   "i32": torch.int32, "device": torch._C._cuda_getDevice, "stream": torch._C._cuda_getCurrentRawStream})
-    return _TYPES
+def _load_parts():
+    """The compiled marshalling and the addresses of _PARTS."""
+    global _parts
+    if _parts is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries come first)
+        from . import build
+        L = lib()
+        if not os.path.exists(build.BINDING):
+            build.build(variant=VARIANT)
+        spec = importlib.util.spec_from_file_location("_binding", build.BINDING)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _parts = (module, *[C.cast(getattr(L, name), C.c_void_p).value for name in _PARTS])
+    return _parts
 
 
-def _rows(t, name: str, n: int, width: int) -> bytes:
-    """dfssm_rows of a 2-D tensor view [n, width] whose rows are contiguous."""
-    step = t.stride()
-    dtype = _TYPES.get(t.dtype) if _TYPES else _init_types().get(t.dtype)
-    if t.shape != (n, width) or (step[1] != 1 and width > 1) or dtype is None:
-        raise ValueError(f"{name} must be float16 or float32 [{n}, {width}] with contiguous rows, not {t.dtype} "
-                         f"{tuple(t.shape)} with strides {step}")
-    return _ROWS(t.data_ptr(), step[0] if n > 1 else max(step[0], width), dtype)
-
-
-def _at(t, name: str, dtype: str, *shape) -> int:
-    """Address of a contiguous tensor of this type and shape; 0 for None."""
-    if t is None:
-        return 0
-    if t.dtype is not (_TYPES or _init_types())[dtype] or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {_TYPES[dtype]} tensor of shape {shape}, not {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
-    return t.data_ptr()
-
-
-def _seqs(n_rows: int, start, slot, fresh, status, slots: int) -> bytes:
-    n = n_rows if start is None else start.shape[0] - 1
-    if n < 0:
-        raise ValueError("start must hold one more entry than there are sequences")
-    return _SEQS(n, n_rows, slots, _at(start, "start", "i32", n + 1), _at(slot, "slot", "i32", n),
-                 _at(fresh, "fresh", "i32", n), _at(status, "status", "i32", 1))
-
-
-def _call(fn, tensors, stream, *args) -> None:
-    """fn(*args, stream) on the device that all the tensors lie on."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            dev = -1
-    if dev < 0:
-        raise ValueError("all tensors must lie on one CUDA device")
-    if dev != _TYPES["device"]():
-        import torch
-        with torch.cuda.device(dev):
-            return _call(fn, tensors, stream, *args)
-    rc = fn(*args, _TYPES["stream"](dev) if stream is None else stream.cuda_stream)
-    if rc != OK:
-        raise DfssmError(rc, last_error())
-
-
-def _conv(fn, x, w, b, state, y, start, slot, fresh, silu, status, stream) -> None:
-    n, c = x.shape
-    width = w.shape[1]
-    slots = 0 if state is None else state.shape[0]
-    _call(fn, (x, w, b, state, y, start, slot, fresh, status), stream, c, width, int(silu), _rows(x, "x", n, c),
-          _at(w, "w", "f16", c, width), _at(b, "b", "f16", c),
-          _seqs(n, start, slot, fresh, status, slots), _at(state, "state", "f32", slots, width - 1, c),
-          _rows(y, "y", n, c))
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def conv_prompt(x, w, b, state, y, start, slot=None, fresh=None, silu=True, status=None, stream=None) -> None:
@@ -521,36 +494,27 @@ def conv_prompt(x, w, b, state, y, start, slot=None, fresh=None, silu=True, stat
     fp32, rows may be strided), w fp16 [channels, d_conv], b fp16 [channels] or None, state
     fp32 [slots, d_conv - 1, channels] or None, start int32 [seqs + 1], slot and fresh
     int32 [seqs] or None, status int32 [1] or None."""
-    _conv(lib().dfssm_conv_prompt, x, w, b, state, y, start, slot, fresh, silu, status, stream)
+    m = _parts or _load_parts()
+    if start is None:
+        raise ValueError("conv_prompt needs start (conv_token takes single tokens)")
+    rc = m[0].conv(m[1], x, w, b, state, y, start, slot, fresh, silu, status, _raw(stream))
+    if rc != OK:
+        raise DfssmError(rc, last_error())
 
 
 def conv_token(x, w, b, state, y, slot=None, fresh=None, silu=True, status=None, stream=None) -> None:
     """One conv step of every sequence (dfssm_conv_token); arguments as conv_prompt's."""
-    _conv(lib().dfssm_conv_token, x, w, b, state, y, None, slot, fresh, silu, status, stream)
-
-
-def _scan_struct(B, dt_bias, A_log, D, state, headdim, groups) -> Tuple[bytes, int, int, int]:
-    """dfssm_scan, and the widths of x and B and the number of slots."""
-    H = dt_bias.shape[0]
-    dtype, slots = DTYPE_F32, 0
-    if state is not None:
-        slots, heads, P, N = state.shape
-        dtype = (_TYPES or _init_types()).get(state.dtype)
-        if dtype is None or heads != H or not state.is_contiguous():
-            raise ValueError("state must be a contiguous fp32 or fp16 tensor [slots, heads, headdim, d_state]")
-        groups = B.shape[1] // max(N, 1)
-    elif headdim and groups:
-        P, N = headdim, B.shape[1] // groups
-    else:
-        raise ValueError("without a state, headdim and groups must be given")
-    return (_SCAN(H, P, N, groups, dtype, _at(dt_bias, "dt_bias", "f32", H), _at(A_log, "A_log", "f32", H),
-                  _at(D, "D", "f32", H)), H * P, groups * N, slots)
+    m = _parts or _load_parts()
+    rc = m[0].conv(m[2], x, w, b, state, y, None, slot, fresh, silu, status, _raw(stream))
+    if rc != OK:
+        raise DfssmError(rc, last_error())
 
 
 def scan_workspace_bytes(nheads: int, headdim: int, d_state: int, groups: int, n_seqs: int, n_rows: int,
                          half: bool = False) -> int:
-    s = _SCAN(nheads, headdim, d_state, groups, DTYPE_F32, 0, 0, 0)
-    n = int(lib().dfssm_scan_workspace_bytes(s, DTYPE_F16 if half else DTYPE_F32, n_seqs, n_rows))
+    """dfssm_scan_workspace_bytes for x, B and C rows of fp16 (half) or fp32."""
+    s = CScan(nheads, headdim, d_state, groups, DTYPE_F32, None, None, None)
+    n = int(lib().dfssm_scan_workspace_bytes(C.byref(s), DTYPE_F16 if half else DTYPE_F32, n_seqs, n_rows))
     if n == 0:
         raise DfssmError(ERR_INVALID_ARG, last_error())
     return n
@@ -564,16 +528,6 @@ def scan_workspace(x, state, n_seqs: int, groups: int = 1):
     return torch.empty(n, dtype=torch.uint8, device=x.device)
 
 
-def _scan(fn, x, dt, B, Cm, dt_bias, A_log, D, state, y, start, slot, fresh, status, stream, ws, headdim, groups):
-    n = x.shape[0]
-    s, E, GN, slots = _scan_struct(B, dt_bias, A_log, D, state, headdim, groups)
-    args = (s, _rows(x, "x", n, E), _rows(dt, "dt", n, dt_bias.shape[0]), _rows(B, "B", n, GN), _rows(Cm, "C", n, GN),
-            _seqs(n, start, slot, fresh, status, slots), _ptr(state), _rows(y, "y", n, E))
-    if ws is not None:
-        args += (ws.data_ptr(), ws.numel() * ws.element_size())
-    _call(fn, (x, dt, B, Cm, dt_bias, A_log, D, state, y, start, slot, fresh, status, ws), stream, *args)
-
-
 def scan_prompt(x, dt, B, C, dt_bias, A_log, D, state, y, start, ws, slot=None, fresh=None, status=None, stream=None,
                 headdim=None, groups=None) -> None:
     """Selective scan over packed prompts (dfssm_scan_prompt): x, y [rows, heads * headdim],
@@ -581,31 +535,38 @@ def scan_prompt(x, dt, B, C, dt_bias, A_log, D, state, y, start, ws, slot=None, 
     may be strided), dt_bias, A_log, D fp32 [heads] (D may be None), state fp32 or fp16
     [slots, heads, headdim, d_state] or None (then headdim and groups say the shape), ws from
     scan_workspace; start, slot, fresh, status as conv_prompt's."""
-    _scan(lib().dfssm_scan_prompt, x, dt, B, C, dt_bias, A_log, D, state, y, start, slot, fresh, status, stream, ws,
-          headdim, groups)
+    m = _parts or _load_parts()
+    if start is None:
+        raise ValueError("scan_prompt needs start (scan_token takes single tokens)")
+    rc = m[0].scan(m[3], x, dt, B, C, dt_bias, A_log, D, state, y, start, ws, slot, fresh, status, headdim, groups,
+                   _raw(stream))
+    if rc != OK:
+        raise DfssmError(rc, last_error())
 
 
 def scan_token(x, dt, B, C, dt_bias, A_log, D, state, y, slot=None, fresh=None, status=None, stream=None) -> None:
     """One scan step of every sequence (dfssm_scan_token); arguments as scan_prompt's."""
-    _scan(lib().dfssm_scan_token, x, dt, B, C, dt_bias, A_log, D, state, y, None, slot, fresh, status, stream, None,
-          None, None)
+    m = _parts or _load_parts()
+    rc = m[0].scan(m[4], x, dt, B, C, dt_bias, A_log, D, state, y, None, None, slot, fresh, status, None, None,
+                   _raw(stream))
+    if rc != OK:
+        raise DfssmError(rc, last_error())
 
 
 def gated_norm(y, z, w, out, groups: int = 1, stream=None) -> None:
     """out = rmsnorm(y * silu(z)) * w over each of `groups` parts of a row (dfssm_gated_norm);
     z None: no gate.  y, z, out [rows, cols] fp16 or fp32, w fp16 [cols]."""
-    n, c = y.shape
-    _call(lib().dfssm_gated_norm, (y, z, w, out), stream, n, c, groups, _rows(y, "y", n, c),
-          None if z is None else _rows(z, "z", n, c), _at(w, "w", "f16", c), _rows(out, "out", n, c))
+    m = _parts or _load_parts()
+    rc = m[0].gated_norm(m[5], y, z, w, out, groups, _raw(stream))
+    if rc != OK:
+        raise DfssmError(rc, last_error())
 
 
 def dense_forward(w, x, y, bias=None, residual=None, silu=False, status=None, stream=None) -> None:
     """y = act(x w^T + bias) + residual (dfssm_dense_forward): w fp16 [rows, cols], x fp16
     [batch, cols], bias fp16 [rows] or None, y and residual fp16 or fp32 [batch, rows]; y may be the
     residual itself."""
-    rows, cols = w.shape
-    n = x.shape[0]
-    _call(lib().dfssm_dense_forward, (x, w, bias, residual, y, status), stream, rows, cols, n, _at(w, "w", "f16", rows, cols),
-          _at(bias, "bias", "f16", rows), int(silu), _rows(x, "x", n, cols),
-          None if residual is None else _rows(residual, "residual", n, rows), _rows(y, "y", n, rows),
-          _at(status, "status", "i32", 1))
+    m = _parts or _load_parts()
+    rc = m[0].dense_forward(m[6], w, x, y, bias, residual, silu, status, _raw(stream))
+    if rc != OK:
+        raise DfssmError(rc, last_error())

@@ -16,15 +16,15 @@ NULL = None
 
 
 def rows(ptr=FAKE, stride=1 << 20, dtype=F.DTYPE_F32):
-    return F._ROWS(ptr, stride, dtype)
+    return C.byref(F.CRows(ptr, stride, dtype))
 
 
 def seqs(n=2, r=8, slots=4, start=FAKE, slot=FAKE, fresh=0, status=0):
-    return F._SEQS(n, r, slots, start, slot, fresh, status)
+    return C.byref(F.CSeqs(n, r, slots, start, slot, fresh, status))
 
 
 def scan(h=8, p=64, n=16, g=1, st=F.DTYPE_F32, bias=FAKE, a=FAKE, d=FAKE):
-    return F._SCAN(h, p, n, g, st, bias, a, d)
+    return C.byref(F.CScan(h, p, n, g, st, bias, a, d))
 
 
 def expect(code, rc, text):
@@ -150,18 +150,23 @@ def test_norm_and_dense_refusals():
 
 
 def test_binding_refuses_before_the_library_is_called():
+    """Shapes, types and devices, checked before any pointer is taken (host tensors here: the
+    device is looked at last)."""
     import torch
-    x = torch.zeros(4, 8)
-    for bad in (torch.zeros(4, 9), torch.zeros(3, 8), torch.zeros(8, 4).t(), torch.zeros(4, 8, dtype=torch.float64)):
-        with pytest.raises(ValueError):
-            F._rows(bad, "x", 4, 8)
-    assert F._rows(x[:1], "x", 1, 8)
-    with pytest.raises(ValueError):
-        F.gated_norm(x, x, torch.zeros(8, dtype=torch.float16), x)      # host tensors
-    with pytest.raises(ValueError):
-        F.gated_norm(x, x, torch.zeros(8), x)                            # w must be fp16
-    with pytest.raises(ValueError):
-        F.conv_token(x, torch.zeros(8, 4).half(), None, torch.zeros(4, 2, 8), x)   # state of another width
+    x, w = torch.zeros(4, 8), torch.zeros(8, dtype=torch.float16)
+
+    def no(text, fn, *args, **kw):
+        with pytest.raises(ValueError, match=text):
+            fn(*args, **kw)
+    for other in (torch.zeros(4, 9), torch.zeros(3, 8), torch.zeros(8, 4).t(), torch.zeros(4, 8, dtype=torch.float64)):
+        no("CUDA|out must", F.gated_norm, x, x, w, other)
+    no("CUDA device", F.gated_norm, x, x, w, x)
+    no("matri", F.gated_norm, x[0], x, w, x)
+    no("CUDA", F.conv_token, x, torch.zeros(8, 4).half(), None, torch.zeros(4, 3, 8), x)
+    no("start", F.conv_prompt, x, torch.zeros(8, 4).half(), None, torch.zeros(4, 3, 8), x, None)
+    no("headdim", F.scan_prompt, x, x, x, x, torch.zeros(1), torch.zeros(1), None, None, x, torch.zeros(2).int(), x)
+    no("state", F.scan_token, x, x, x, x, torch.zeros(1), torch.zeros(1), None, torch.zeros(2, 2, 8, 8), x)
+    no("CUDA", F.dense_forward, torch.zeros(8, 8).half(), x, x)
 
 
 def test_live_sequences():
