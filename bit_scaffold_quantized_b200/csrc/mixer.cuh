@@ -136,7 +136,9 @@ DFSSM_DEV void split_h2(float a, float b, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(a, b);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   const float2 f = __half22float2(h);
-  lo = pack_h2(a - f.x, b - f.y);
+  float l0, l1;
+  fma2(l0, l1, f.x, f.y, -1.f, -1.f, a, b);
+  lo = pack_h2(l0, l1);
 }
 
 // v / (1 + e^-v) in five instructions: the rounding of v log2 e and the two approximate

@@ -27,11 +27,12 @@ namespace dfssm {
 //                (W) or of the state's columns (S, H; in registers throughout).  Their
 //                latencies are what bounds the kernel: with half as many warps of twice the
 //                work it issued 0.36 instructions per cycle and scheduler;
-//   warp 16      TMA: B double-buffered, C and X single (each is asked for again as soon
+//   warps 16, 17 a head each: the chunk's largest |x|, W's factors, the scales (on the
+//                schedulers whose warps hold the fewest columns of M);
+//   warp 18      TMA: B double-buffered, C and X single (each is asked for again as soon
 //                as its last reader is done, a good part of a chunk before it is needed;
 //                without C there is room for two X);
-//   warp 17      MMA issuer;
-//   warps 18, 19 a head each: the chunk's largest |x|, W's factors, the scales.
+//   warp 19      MMA issuer.
 // k_scan_steps goes before: the step sizes, their running sums (fp64) and the tables of
 // every chunk and head.  cs is kept as two floats, hi + lo: near differences are then good to
 // 2^-24 of their own size however far the sum has run (a step may be huge).
@@ -46,6 +47,7 @@ namespace dfssm {
 constexpr int kStWarps = 16;                   // of the arithmetic
 constexpr int kStCompute = 32 * kStWarps;
 constexpr int kStThreads = kStCompute + 128;
+constexpr int kStTma = kStWarps + 2, kStMma = kStWarps + 3;
 constexpr int kStP = 64;
 
 __host__ __device__ constexpr int st_tile_bytes(int n) { return kStQ * n * 2; }
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   unsigned char* const sH = sC + (STATES ? 0 : TB);                  // [2 heads][hi, lo][halves][64 rows][128 B]
   float* const tab = reinterpret_cast<float*>(sH + st_h_bytes(N, STATES));   // [2][2][kStTab]
 
-  if (warp == kStWarps + 1) {
+  if (warp == kStMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(&tmem_s)), "n"(COLS) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   const int chunks = work ? (w.t1 - w.t0 + kStQ - 1) / kStQ : 0;
   const int chunk0 = work ? w.b / kStQ + w.s + (w.t0 - w.b) / kStQ : 0;      // number of the first
 
-  if (warp == kStWarps) {
+  if (warp == kStTma) {
     // ---- TMA
     const bool one = elect_one();
     int issued = 0;
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
     }
     for (int c = max(0, issued - XB); c < issued; ++c) landed(bars.fullX[c % XB], c / XB);
     if (!STATES && issued > 0) landed(bars.fullC, issued - 1);
-  } else if (warp == kStWarps + 1) {
+  } else if (warp == kStMma) {
     // ---- MMA
     const bool one = elect_one();
     const uint32_t i1 = umma_idesc_f16(128, 128), i2 = umma_idesc_f16(128, kStP, true), i3 = umma_idesc_f16(128, kStP),
@@ -373,9 +375,9 @@ __global__ void __launch_bounds__(kStThreads, 1)
       for (long long s = 0; s < kTcSpinLimit && !mbar_try_wait(&bars.done, 0u); ++s) {
       }
     }
-  } else if (warp >= kStWarps + 2) {
+  } else if (warp >= kStWarps) {
     // ---- scales of head h0 + hd
-    const int hd = warp - kStWarps - 2, h = h0 + hd;
+    const int hd = warp - kStWarps, h = h0 + hd;
     const float Dh = chunks && a.D ? fabsf(a.D[h]) : 0.f;
     const float* big = a.big + (size_t(chunk0) * a.G + g) * 2;
     float bnext = chunks ? big[0] : 0.f, cnext = chunks ? big[1] : 0.f, total = 0.f, hmost = 0.f;
@@ -488,7 +490,11 @@ __global__ void __launch_bounds__(kStThreads, 1)
       for (int j = 0; j < NH; j += 8) {
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split_h2(hs[j + 2 * i] * up, hs[j + 2 * i + 1] * up, hi[i], lo[i]);
+        for (int i = 0; i < 4; ++i) {
+          float h0, h1;
+          mul2(h0, h1, hs[j + 2 * i], hs[j + 2 * i + 1], up, up);
+          split_h2(h0, h1, hi[i], lo[i]);
+        }
         const int n = NH * wg + j;
         unsigned char* at = sH + (n >> 6) * 8192 + p * 128 + ((((n & 63) >> 3) ^ (p & 7)) << 4) + 2 * hd * kStP * N * 2;
         *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -525,8 +531,8 @@ __global__ void __launch_bounds__(kStThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          hs[j + i] = fmaf(hs[j + i], keep, v[i] * down);
-          hs[j + i + 1] = fmaf(hs[j + i + 1], keep, v[i + 1] * down);
+          mul2(v[i], v[i + 1], v[i], v[i + 1], down, down);
+          fma2(hs[j + i], hs[j + i + 1], hs[j + i], hs[j + i + 1], keep, keep, v[i], v[i + 1]);
         }
       }
       tc_fence_before();
@@ -577,10 +583,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
                 const float4 cf = *reinterpret_cast<const float4*>(te + kStCol + s0 + i);
-                v[i] = (v[i] * f) * cf.x;
-                v[i + 1] = (v[i + 1] * f) * cf.y;
-                v[i + 2] = (v[i + 2] * f) * cf.z;
-                v[i + 3] = (v[i + 3] * f) * cf.w;
+                mul2(v[i], v[i + 1], v[i], v[i + 1], f, f);
+                mul2(v[i + 2], v[i + 3], v[i + 2], v[i + 3], f, f);
+                mul2(v[i], v[i + 1], v[i], v[i + 1], cf.x, cf.y);
+                mul2(v[i + 2], v[i + 3], v[i + 2], v[i + 3], cf.z, cf.w);
               }
             } else {
 #pragma unroll
@@ -632,8 +638,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             x[j] = __half2float(*reinterpret_cast<const __half*>(xc + (i + j) * 128 + ((ch ^ ((i + j) & 7)) << 4)));
-          split_h2(x[0] * f.x, x[1] * f.y, hi[i / 2], lo[i / 2]);
-          split_h2(x[2] * f.z, x[3] * f.w, hi[i / 2 + 1], lo[i / 2 + 1]);
+          mul2(x[0], x[1], x[0], x[1], f.x, f.y);
+          mul2(x[2], x[3], x[2], x[3], f.z, f.w);
+          split_h2(x[0], x[1], hi[i / 2], lo[i / 2]);
+          split_h2(x[2], x[3], hi[i / 2 + 1], lo[i / 2 + 1]);
         }
         if (!STATES) {
           wait(bars.ydone, c);               // M of head 1 has been read
@@ -659,7 +667,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
           tmem_ld16(tl + cY + 64 * hy + 32 * part + j, y2);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) out[i] = fmaf(y2[i], f2, y1[i] * f1);
+          for (int i = 0; i < 16; i += 2) {
+            mul2(y1[i], y1[i + 1], y1[i], y1[i + 1], f1, f1);
+            fma2(out[i], out[i + 1], y2[i], y2[i + 1], f2, f2, y1[i], y1[i + 1]);
+          }
 #pragma unroll
           for (int i = 0; i < 16; i += E) {
             const int ch = (32 * part + j + i) / E;
@@ -702,7 +713,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kStWarps + 1)
+  if (warp == kStMma)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(COLS) : "memory");
 }
 
