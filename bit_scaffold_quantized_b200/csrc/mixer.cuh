@@ -263,8 +263,11 @@ DFSSM_DEV int conv_edge(const Seqs& q, int t) {
 
 // One block: a.tile rows of kConvThreads * VEC channels; a thread walks its channels down the
 // rows with the last W - 1 inputs in registers.  The tile is such that the blocks come in
-// whole waves over the SMs: 24 packed prompts, 6007 rows of 4352 channels, fp32 to fp16, 39 us
-// (tiles of 32: 40, of 64: 47).
+// whole waves over the SMs.  Each row's load goes out as the row kConvUnroll before it is done.
+// 24 packed prompts, 6007 rows of 4352 channels, fp32 to fp16: 36.8 us, 4.3 TB/s (loads in
+// groups that are waited for: 38.5; five or six rows ahead spill: 52; three: 38; tiles of 64 rows: 47).
+// It is bound by latency: of ten cycles a warp waits four for its loads, and a
+// block's first rows wait for the sequence's bounds, its slot and the weights.
 template <typename TX, typename TY, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads, kConvBlocks) k_conv_prompt(ConvArgs a) {
   pdl_wait();
@@ -338,11 +341,11 @@ __global__ void __launch_bounds__(kConvThreads, kConvBlocks) k_conv_prompt(ConvA
         }
       }
     }
-    while (r < stop) {
-      float x[kConvUnroll][VEC], v[VEC];
+    float x[kConvUnroll][VEC], v[VEC];
 #pragma unroll
-      for (int u = 0; u < kConvUnroll; ++u)
-        if (r + u < stop) ldv<VEC>(xp + (long long)(r + u) * a.x.stride, x[u]);
+    for (int u = 0; u < kConvUnroll; ++u)
+      if (r + u < stop) ldv<VEC>(xp + (long long)(r + u) * a.x.stride, x[u]);
+    while (r < stop) {
 #pragma unroll
       for (int u = 0; u < kConvUnroll; ++u) {
         if (r + u < stop) {
@@ -354,6 +357,7 @@ __global__ void __launch_bounds__(kConvThreads, kConvBlocks) k_conv_prompt(ConvA
             for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
             win[W - 2][i] = x[u][i];
           }
+          if (r + u + kConvUnroll < stop) ldv<VEC>(xp + (long long)(r + u + kConvUnroll) * a.x.stride, x[u]);
         }
       }
       r += kConvUnroll;
