@@ -101,6 +101,7 @@ int conv(int channels, int d_conv, int silu, const dfssm_rows* x, const uint16_t
   REQUIRE(d_conv >= 2 && d_conv <= 4, DFSSM_ERR_UNSUPPORTED_SHAPE, "d_conv (%d) must be 2, 3 or 4", d_conv);
   int rc;
   if ((rc = check_rows(x, "x", channels)) || (rc = check_rows(y, "y", channels))) return rc;
+  REQUIRE(x->data != y->data, DFSSM_ERR_INVALID_ARG, "y may not be the rows of x");
   REQUIRE_PTR(w);
   REQUIRE(b == nullptr || aligned16(b), DFSSM_ERR_MISALIGNED, "b is not 16-byte aligned");
   if (token) REQUIRE(state != nullptr, DFSSM_ERR_INVALID_ARG, "conv_state is NULL");
@@ -210,6 +211,8 @@ int check_scan_call(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* 
   if ((rc = check_rows(x, "x", E)) || (rc = check_rows(dt, "dt", s->nheads)) || (rc = check_rows(B, "B", GN)) ||
       (rc = check_rows(C, "C", GN)) || (rc = check_rows(y, "y", E)))
     return rc;
+  const dfssm_rows* in[] = {x, dt, B, C};
+  for (const dfssm_rows* r : in) REQUIRE(r->data != y->data, DFSSM_ERR_INVALID_ARG, "y may not be the rows of an input");
   REQUIRE(x->dtype == B->dtype && x->dtype == C->dtype, DFSSM_ERR_INVALID_ARG, "x, B and C must have one dtype");
   REQUIRE_PTR(s->dt_bias);
   REQUIRE_PTR(s->A_log);
@@ -268,8 +271,8 @@ int join_blocks(const ScanArgs& a) {
 template <typename TX, typename TY, typename TS>
 int scan_prompt_launch(const ScanArgs& a, cudaStream_t st) {
   const size_t smem = scan_smem_bytes(a.P, a.N);
-  auto attr = [&](auto kernel) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  auto attr = [&](auto kernel) {         // the same limit in every call: two may run at once
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(scan_smem_bytes(128, 256)));
   };
   cudaError_t e = attr(k_scan_prompt<TX, TY, TS, false>);
   if (e == cudaSuccess) e = attr(k_scan_prompt<TX, TY, TS, true>);
@@ -463,7 +466,8 @@ int dense_tc(DenseArgs a, cudaStream_t st) {
   const int pairs = std::min(a.tiles, dense_clusters(t.ks));
   return by_dense_types(a, [&](auto* ty, auto* tr) {
     const auto kernel = k_dense_tc<std::remove_pointer_t<decltype(ty)>, std::remove_pointer_t<decltype(tr)>>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // the same limit in every call: two may run at once
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kDtSmemCap));
     if (e != cudaSuccess) return fail(DFSSM_ERR_CUDA, "k_dense_tc smem attribute: %s", cudaGetErrorString(e));
     CHAIN_LAUNCH("k_dense_tc", kernel, dim3(2 * pairs, 1, t.ks), dim3(kDtThreads), smem, st, dim3(2, 1, t.ks), a, tw, tx);
     return int(DFSSM_OK);
@@ -478,7 +482,7 @@ int dense_few(const DenseArgs& a, cudaStream_t st) {
   const size_t smem = df_smem_bytes(NT, warps);
   return by_dense_types(a, [&](auto* ty, auto* tr) {
     const auto kernel = k_dense_few<std::remove_pointer_t<decltype(ty)>, std::remove_pointer_t<decltype(tr)>, NT>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(df_smem_bytes(NT, 16)));
     if (e != cudaSuccess) return fail(DFSSM_ERR_CUDA, "k_dense_few smem attribute: %s", cudaGetErrorString(e));
     CHAIN_LAUNCH("k_dense_few", kernel, dim3(gx, gy), dim3(32 * warps), smem, st, 0, a);
     return int(DFSSM_OK);
@@ -619,6 +623,7 @@ int dfssm_dense_forward(int rows, int cols, int batch, const uint16_t* w, const 
   REQUIRE(aligned16(b), DFSSM_ERR_MISALIGNED, "b is not 16-byte aligned");
   int rc;
   if ((rc = check_rows(x, "x", cols, true)) || (rc = check_rows(y, "y", rows))) return rc;
+  REQUIRE(x->data != y->data, DFSSM_ERR_INVALID_ARG, "y may not be the rows of x");
   if (residual) {
     if ((rc = check_rows(residual, "residual", rows))) return rc;
     REQUIRE(residual->data != y->data || (residual->dtype == y->dtype && residual->stride == y->stride),

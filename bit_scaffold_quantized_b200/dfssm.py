@@ -523,8 +523,9 @@ def scan_workspace_bytes(nheads: int, headdim: int, d_state: int, groups: int, n
 def scan_workspace(x, state, n_seqs: int, groups: int = 1):
     """Workspace tensor for scan_prompt on rows like x with states like state."""
     import torch
-    n = scan_workspace_bytes(state.shape[1], state.shape[2], state.shape[3], groups, n_seqs, x.shape[0],
-                             x.dtype == torch.float16)
+    with torch.cuda.device(x.device):        # the size depends on the device
+        n = scan_workspace_bytes(state.shape[1], state.shape[2], state.shape[3], groups, n_seqs, x.shape[0],
+                                 x.dtype == torch.float16)
     return torch.empty(n, dtype=torch.uint8, device=x.device)
 
 
