@@ -127,6 +127,10 @@ DFSSM_DEV float exp2_f(float v) {
 
 DFSSM_DEV float pow2_f(int k) { return __int_as_float((k + 127) << 23); }       // |k| <= 126
 // k with v 2^k in [2^13, 2^14) (0 for v = 0, and within [-80, 80]).
+DFSSM_DEV float finite_abs(float v) {        // 0 where v is no number: bounds are of the others
+  v = fabsf(v);
+  return v <= 3.402823466e38f ? v : 0.f;
+}
 DFSSM_DEV int scale_of(float v) {
   const int e = int((__float_as_uint(v) >> 23) & 0xffu) - 126;                    // v < 2^e
   return v > 0.f ? max(-80, min(80, 14 - e)) : 0;
@@ -664,7 +668,8 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_prompt(ScanArgs a) {
         for (int s = 0; s < 4 * warp + 4; ++s) {
           const float xv = xs[s * P + p];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[k] = fmaf(ms[(4 * warp + k) * (Q + 4) + s], xv, acc[k]);
+          for (int k = 0; k < 4; ++k)       // a later row's x may be no number: 0 times it is none
+            if (s <= 4 * warp + k) acc[k] = fmaf(ms[(4 * warp + k) * (Q + 4) + s], xv, acc[k]);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

@@ -53,7 +53,7 @@ DFSSM_DEV void load4(const Rows& r, long long row, int col, int width, bool vec,
 }
 DFSSM_DEV float finite_top(float m, const float (&v)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(v[i]) < 3e38f ? fabsf(v[i]) : 0.f);
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, finite_abs(v[i]));
   return m;
 }
 // Four values, scaled, as fp16 pieces at hi (and hi + lo_at).
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
   __half* const Cs = Ms + 2 * Q * kSmXS;                            // [PIECES][Q][SN]
   __half* const Hs = Cs + PIECES * Q * SN;                          // [2][kSmP][SN]
   __shared__ __align__(16) float hi_s[Q], lo_s[Q], dt_s[Q], w_s[Q], red[4][16], sums[3];      // sums: exp(cs_Q), max dt, max w
+  __shared__ int first[kSmP];           // first row of the chunk whose x is no number, by p
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, t4 = lane & 3;
   const int P = a.P, N = a.N, h = blockIdx.y, g = h / (a.H / a.G);
   SegWork w;
@@ -211,10 +212,10 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
         const double v = __shfl_up_sync(0xffffffffu, up, o);
         if (lane >= o) up += v;
       }
-      const double total = __shfl_sync(0xffffffffu, up, 31), before = up - cs[1];
+      const double total = __shfl_sync(0xffffffffu, up, 31), left = __shfl_up_sync(0xffffffffu, up, 1);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        cs[j] += before;
+        cs[j] += lane ? left : 0.0;
         const double e = cs[j] * log2e;
         const float hi = float(e);
         hi_s[2 * lane + j] = hi;
@@ -223,7 +224,8 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
         wf[j] = exp2_f(float((total - cs[j]) * log2e)) * dt[j];
         w_s[2 * lane + j] = wf[j];
       }
-      const float dmax = warp_max(fmaxf(dt[0], dt[1])), wmax = warp_max(fmaxf(wf[0], wf[1]));
+      const float dmax = warp_max(fmaxf(finite_abs(dt[0]), finite_abs(dt[1]))),
+                  wmax = warp_max(fmaxf(finite_abs(wf[0]), finite_abs(wf[1])));
       total_log2 += total * log2e;
       if (lane == 0) {
         sums[0] = exp2_f(float(total * log2e));
@@ -231,7 +233,12 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
         sums[2] = wmax;
       }
     }
-    __syncthreads();
+    bool odd = false;                       // an x that is no number
+#pragma unroll
+    for (int i = 0; i < GX; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) odd |= !(fabsf(vx[i][j]) <= 3.402823466e38f);
+    odd = __syncthreads_or(odd) != 0;
     const float xt = red_top(0), bt = red_top(1), ct = STATES ? 0.f : red_top(2), keep = sums[0];
     const float xup = PIECES == 2 ? pow2_f(scale_of(xt)) : 1.f, bup = PIECES == 2 ? pow2_f(scale_of(bt)) : 1.f,
                 cup = PIECES == 2 ? pow2_f(scale_of(ct)) : 1.f;
@@ -239,8 +246,26 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
 #pragma unroll
     for (int i = 0; i < GX; ++i) {
       const int e = tid + i * kSmThreads, t = e / (kSmP / 4), c = 4 * (e % (kSmP / 4));
-      if (!STATES) store4<PIECES>(Xs + t * kSmXS + c, Q * kSmXS, vx[i], xup);
       store4<2>(Ws + t * kSmXS + c, Q * kSmXS, vx[i], w_s[t] * wup);
+      if (!STATES && !odd) store4<PIECES>(Xs + t * kSmXS + c, Q * kSmXS, vx[i], xup);
+    }
+    if (!STATES && odd) {
+      // M is zero for later rows, but 0 times no number is none: such an x counts as zero
+      // in M X, and y of its row and the later ones is made no number where it is stored
+      if (tid < kSmP) first[tid] = Q;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < GX; ++i) {
+        const int e = tid + i * kSmThreads, t = e / (kSmP / 4), c = 4 * (e % (kSmP / 4));
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool fine = fabsf(vx[i][j]) <= 3.402823466e38f;
+          v[j] = fine ? vx[i][j] : 0.f;
+          if (!fine) atomicMin(&first[c + j], t);
+        }
+        store4<PIECES>(Xs + t * kSmXS + c, Q * kSmXS, v, xup);
+      }
     }
 #pragma unroll
     for (int i = 0; i < GN; ++i) {
@@ -317,8 +342,13 @@ __global__ void __launch_bounds__(kSmThreads) k_scan_mma(ScanArgs a) {
         for (int i = 0; i < 2; ++i) {
           const int p = 16 * part + 8 * i + 2 * t4;
           if (t < n && p < P) {
-            stf(yp + p, fmaf(y2[i][j], et, y1[i][j] * f1));
-            stf(yp + p + 1, fmaf(y2[i][j + 1], et, y1[i][j + 1] * f1));
+            float v0 = fmaf(y2[i][j], et, y1[i][j] * f1), v1 = fmaf(y2[i][j + 1], et, y1[i][j + 1] * f1);
+            if (odd) {
+              if (t >= first[p]) v0 = nanf("");
+              if (t >= first[p + 1]) v1 = nanf("");
+            }
+            stf(yp + p, v0);
+            stf(yp + p + 1, v1);
           }
         }
       }

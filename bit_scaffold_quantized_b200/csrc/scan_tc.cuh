@@ -27,7 +27,8 @@ namespace dfssm {
 //                (W) or of the state's columns (S, H; in registers throughout).  Their
 //                latencies are what bounds the kernel: with half as many warps of twice the
 //                work it issued 0.36 instructions per cycle and scheduler;
-//   warps 16, 17 a head each: the chunk's largest |x|, W's factors, the scales (on the
+//   warps 16, 17 a head each: the chunk's largest |x|, what to do with one that is no
+//                number, W's factors, the scales (on the
 //                schedulers whose warps hold the fewest columns of M);
 //   warp 18      TMA: B double-buffered, C and X single (each is asked for again as soon
 //                as its last reader is done, a good part of a chunk before it is needed;
@@ -120,8 +121,9 @@ __global__ void __launch_bounds__(256) k_scan_steps(ScanArgs a) {
       if (lane >= o) up += v;
     }
     const double total = __shfl_sync(0xffffffffu, up, 31);
+    const double left = __shfl_up_sync(0xffffffffu, up, 1);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cs[j] += up - run;
+    for (int j = 0; j < 4; ++j) cs[j] += lane ? left : 0.0;
     const double last = __shfl_sync(0xffffffffu, cs[3], lane | 7);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -130,8 +132,8 @@ __global__ void __launch_bounds__(256) k_scan_steps(ScanArgs a) {
       lo[j] = float(e - double(hi[j]));
       raw[j] = exp2_f(float((total - cs[j]) * log2e)) * dt[j];
       col[j] = exp2_f(float((last - cs[j]) * log2e)) * dt[j];
-      dmax = fmaxf(dmax, dt[j]);
-      big = fmaxf(big, raw[j]);
+      dmax = fmaxf(dmax, finite_abs(dt[j]));
+      big = fmaxf(big, finite_abs(raw[j]));
     }
     dmax = warp_max(dmax);
     big = warp_max(big);
@@ -201,6 +203,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
   // that leaves the chunk
   __shared__ __align__(16) float scal[2][2][4];
   __shared__ __align__(16) float wmax[2][8], hbig[2];
+  __shared__ int odd[2][2], first[2][2][kStP];     // [buffer][head]: an x is no number; its first row, by p
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -402,27 +405,50 @@ __global__ void __launch_bounds__(kStThreads, 1)
         arrive(bars.tabA[b]);
       }
       wait(bars.fullX[c % XB], c / XB);
-      const unsigned char* xt = sX + (2 * (c % XB) + hd) * TX;
-      const __half2 most = __floats2half2_rn(65504.f, 65504.f);
-      __half2 m[4];                    // chains of their own
+      unsigned char* const xt = sX + (2 * (c % XB) + hd) * TX;
+      auto largest = [&] {
+        __half2 m[4];                    // chains of their own
 #pragma unroll
-      for (int k = 0; k < 4; ++k) m[k] = __floats2half2_rn(0.f, 0.f);
+        for (int k = 0; k < 4; ++k) m[k] = __floats2half2_rn(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = lane + 32 * i;
-        if (r < n) {
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i;
+          if (r < n) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 v = *reinterpret_cast<const uint4*>(xt + r * 128 + ((j ^ (r & 7)) << 4));      // no two of 8 lanes in one bank
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            for (int j = 0; j < 8; ++j) {
+              const uint4 v = *reinterpret_cast<const uint4*>(xt + r * 128 + ((j ^ (r & 7)) << 4));      // no two of 8 lanes in one bank
+              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              m[k] = __hmax2(m[k], __hmin2(__habs2(*reinterpret_cast<const __half2*>(&u[k])), most));
+              for (int k = 0; k < 4; ++k) m[k] = __hmax2_nan(m[k], __habs2(*reinterpret_cast<const __half2*>(&u[k])));
+            }
           }
         }
+        const __half2 mm = __hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3]));
+        return __half2float(__hmax_nan(__low2half(mm), __high2half(mm)));
+      };
+      float xmax = largest();
+      const bool none = __any_sync(0xffffffffu, !(xmax <= 65504.f));
+      if (none) {
+        // M is zero for later rows, but 0 times no number is none: such an x counts as
+        // zero in the products, and y of its row and the later ones and the state are made
+        // no number where they are
+        first[b][hd][lane] = first[b][hd][lane + 32] = kStQ;
+        __syncwarp();
+#pragma unroll 1
+        for (int e = lane; e < n * kStP; e += 32) {
+          const int r = e / kStP, p = e % kStP;
+          uint16_t* at = reinterpret_cast<uint16_t*>(xt + r * 128 + (((p >> 3) ^ (r & 7)) << 4)) + (p & 7);
+          if ((*at & 0x7c00u) == 0x7c00u) {
+            *at = 0;
+            atomicMin(&first[b][hd][p], r);
+          }
+        }
+        __syncwarp();
+        fence_async_smem();
+        xmax = largest();
       }
-      const __half2 mm = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
-      const float xmax = warp_max(fmaxf(__low2float(mm), __high2float(mm)));
+      xmax = warp_max(xmax);
+      if (lane == 0) odd[b][hd] = none;
       const int k = scale_of(xmax * meta.z);
       const float up = pow2_f(k), down = pow2_f(-k);
       const float4 f = *reinterpret_cast<const float4*>(tb + kStRaw + 4 * lane);
@@ -507,7 +533,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
     if (!STATES) {
       float m = 0.f;
 #pragma unroll
-      for (int j = 0; j < NH; ++j) m = fmaxf(m, fabsf(hs[j]));
+      for (int j = 0; j < NH; ++j) m = fmaxf(m, finite_abs(hs[j]));
       m = warp_max(m);
       if (lane == 0) wmax[hd][2 * wg + (q & 1)] = m;
       bar_compute();
@@ -620,6 +646,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
           }
         }
         tmem_wait_st();
+        wait(bars.tabX[b], c >> 1);          // an x that is no number is out of X
         tc_fence_before();
         arrive(bars.mready);
       }
@@ -643,6 +670,7 @@ __global__ void __launch_bounds__(kStThreads, 1)
           split_h2(x[0], x[1], hi[i / 2], lo[i / 2]);
           split_h2(x[2], x[3], hi[i / 2 + 1], lo[i / 2 + 1]);
         }
+        if (odd[b][hd] && first[b][hd][p] < kStQ) hi[0] = 0x7fffu;
         if (!STATES) {
           wait(bars.ydone, c);               // M of head 1 has been read
           tc_fence_after();
@@ -670,6 +698,10 @@ __global__ void __launch_bounds__(kStThreads, 1)
           for (int i = 0; i < 16; i += 2) {
             mul2(y1[i], y1[i + 1], y1[i], y1[i + 1], f1, f1);
             fma2(out[i], out[i + 1], y2[i], y2[i + 1], f2, f2, y1[i], y1[i + 1]);
+          }
+          if (odd[b][hy]) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) out[i] = L >= first[b][hy][32 * part + j + i] ? nanf("") : out[i];
           }
 #pragma unroll
           for (int i = 0; i < 16; i += E) {

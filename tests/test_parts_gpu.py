@@ -305,6 +305,30 @@ def test_scan_and_conv_keep_neighbours_clean(xt, poison):
         assert np.array_equal(host(sd)[s], new[s])
 
 
+@pytest.mark.parametrize("shape,xt,pads", [((4, 64, 128, 1), F16, (0, 0, 0, 0)), ((4, 64, 128, 1), F16, (1, 0, 1, 1)),
+                                           ((4, 64, 128, 1), F32, (0, 0, 0, 0)), ((2, 128, 160, 1), F32, (0, 0, 0, 0)),
+                                           ((2, 48, 20, 2), F16, (0, 0, 0, 0))])
+@pytest.mark.parametrize("name", ["x", "dt", "B", "C"])
+@pytest.mark.parametrize("poison", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("at,rows", [(0, 140), (77, 140), (139, 140), (700, 1500)])
+def test_scan_prompt_no_number_reaches_earlier_rows(shape, xt, pads, name, poison, at, rows):
+    """NaN or infinity at one place of a prompt: the rows before it and the heads, channels and
+    states that do not depend on it are as the recurrence has them, the others no numbers
+    (dt of -inf is a step of 0: all are)."""
+    c = scan_case(rows, shape, xt, F32, F32, 1, 61, decay=0.5)
+    c[name][at, 1] = poison
+    with np.errstate(all="ignore"):
+        y, A, new, newA = scan_oracle(c, [0, rows], None, None)
+    yd, sd = run_scan(c, [0, rows], None, None, F32, xt, True, pads)
+    k = scan_k(shape, rows)
+    assert np.all(np.isfinite(y[:at])) and (name == "dt" and poison < 0) == (np.isfinite(y).all() and np.isfinite(new).all())
+    for got, want, size in ((host(yd), y, A), (host(sd), new, newA)):
+        fine = np.isfinite(want)
+        assert not np.isfinite(got[~fine]).any()
+        size = np.where(fine, size, 0)
+        assert np.all(np.abs(got[fine] - want[fine]) <= (k * U * size + half_step(F32, np.where(fine, want, 0)))[fine])
+
+
 def test_scan_prompt_without_state():
     shape, cuts, rows = (4, 64, 128, 1), [0, 70, 200], 200
     for xt in (F16, F32):
