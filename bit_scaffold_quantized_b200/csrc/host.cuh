@@ -137,7 +137,9 @@ inline int sm_count() {
 }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link against
-// the driver library), looked up once.
+// the driver library), looked up once.  It wants a current context, which a host thread
+// has only after its first call that needs one: setting the thread's device gives it one
+// (and, unlike an allocation, may be done while a stream is being captured).
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -148,6 +150,11 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   });
+  thread_local bool bound = false;
+  if (!bound) {
+    int dev = 0;
+    bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+  }
   return fn;
 }
 

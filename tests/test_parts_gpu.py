@@ -698,3 +698,148 @@ def test_tensors_of_two_devices_are_refused():
     assert torch.allclose(out, y * torch.rsqrt(y.pow(2).mean(-1, keepdim=True) + 1e-5), atol=1e-5)
     with pytest.raises(ValueError):
         F.gated_norm(y, None, w.to("cuda:0"), out)
+
+
+def test_rows_and_slots_beyond_32_bits():
+    """Rows 16 MiB apart and slots far into their pool give the bits of compact ones."""
+    n, S, slots = 300, 2 ** 23 + 8, 65700
+    big = torch.empty(n * S, dtype=F16, device=DEV)              # 2.5e9 values
+    far = lambda at, width: big.as_strided((n, width), (S, 1), at)  # noqa: E731
+    rng = np.random.default_rng(95)
+    c = scan_case(n, (4, 64, 128, 1), F16, F16, F32, 1, 95)
+    near = {k: dev(c[k]) for k in ("x", "dt", "B", "C")}
+    wide_ = {}
+    for i, (k, v) in enumerate(near.items()):
+        wide_[k] = far(512 * i, v.shape[1])
+        wide_[k].copy_(v)
+    pool = torch.empty(slots, 4, 64, 128, device=DEV)            # 2.15e9 values
+    par = [dev(c[k]) for k in ("dt_bias", "A_log", "D")]
+    start = ints([0, n])
+
+    def run(rows, y, state, slot):
+        state[slot].copy_(dev(c["state"])[0])
+        ws = F.scan_workspace(rows["x"], state, 1)
+        F.scan_prompt(*[rows[k] for k in ("x", "dt", "B", "C")], *par, state, y, start, ws, ints([slot]))
+        one = [rows[k][-1:] for k in ("x", "dt", "B", "C")]
+        F.scan_token(*one, *par, state, y[:1], ints([slot]))
+        return y.clone(), state[slot].clone()
+    small = run(near, torch.zeros(n, 256, dtype=F16, device=DEV), torch.zeros(1, 4, 64, 128, device=DEV), 0)
+    y = far(2048, 256)
+    large = run(wide_, y, pool, slots - 50)
+    assert torch.equal(small[0], large[0]) and torch.equal(small[1], large[1])
+    # fp32 rows take another kernel
+    f = {k: v.float() for k, v in near.items()}
+    small = run(f, torch.zeros(n, 256, device=DEV), torch.zeros(1, 4, 64, 128, device=DEV), 0)
+    large = run(f, torch.zeros(n, 256, device=DEV), pool, slots - 50)
+    assert torch.equal(small[0], large[0]) and torch.equal(small[1], large[1])
+    # conv
+    m = 2 ** 31 // 768 + 100
+    cpool = pool.view(-1)[:m * 768].view(m, 3, 256)
+    w, st = dev(rng.normal(size=(256, 4)).astype(np.float16)), dev(rng.normal(size=(1, 3, 256)).astype(np.float32))
+    got = []
+    for x, yy, state, slot in ((near["x"], torch.zeros(n, 256, dtype=F16, device=DEV), st.clone(), 0), (wide_["x"], y, cpool, m - 1)):
+        state[slot].copy_(st[0])
+        F.conv_prompt(x, w, None, state, yy, start, ints([slot]))
+        F.conv_token(x[-1:], w, None, state, yy[:1], ints([slot]))
+        got.append((yy.clone(), state[slot].clone()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    # norm, dense (few rows and many)
+    wn, wd = dev(np.ones(256, np.float16)), dev(rng.normal(size=(256, 256)).astype(np.float16))
+    out = torch.zeros(n, 256, dtype=F16, device=DEV)
+    F.gated_norm(near["x"], None, wn, out)
+    F.gated_norm(wide_["x"], None, wn, y)
+    assert torch.equal(out, y)
+    for k in (n, 20):
+        F.dense_forward(wd, near["x"][-k:], out[-k:])
+        F.dense_forward(wd, wide_["x"][-k:], y[-k:])
+        assert torch.equal(out, y)
+
+
+def test_no_number_stays_in_its_row():
+    """Projections and norms of a batch: rows do not reach each other."""
+    for n in (5, 70):
+        x, w, _, _ = dense_case(n, 200, 512, 96, False, None)
+        x[3, 7] = np.nan
+        y, out = torch.zeros(n, 200, device=DEV), torch.zeros(n, 512, device=DEV)
+        F.dense_forward(dev(w), dev(x), y)
+        F.gated_norm(dev(x), None, dev(np.ones(512, np.float16)), out)
+        for v in (y, out):
+            assert torch.isnan(v[3]).all() and torch.isfinite(v[:3]).all() and torch.isfinite(v[4:]).all()
+
+
+def test_calls_of_two_host_threads():
+    """Calls of different sizes at once, from two threads on streams of their own."""
+    import ctypes as C
+    import threading
+    L = F.lib()
+    jobs, errors = [], []
+    for i, (n, rows, cols) in enumerate([(70, 512, 256), (300, 2048, 1024), (20, 512, 4096), (20, 8512, 256)]):
+        x, w, _, _ = dense_case(n, rows, cols, 97 + i, False, None)
+        jobs.append((dev(w), dev(x), torch.zeros(n, rows, device=DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(mine):
+        for _ in range(50):
+            for w, x, y, s in mine:      # the C call itself: it runs without the interpreter's lock
+                rc = L.dfssm_dense_forward(w.shape[0], w.shape[1], x.shape[0], w.data_ptr(), None, 0,
+                                           C.byref(F.CRows(x.data_ptr(), x.shape[1], F.DTYPE_F16)), None,
+                                           C.byref(F.CRows(y.data_ptr(), y.shape[1], F.DTYPE_F32)), None, s.cuda_stream)
+                if rc != F.OK:
+                    errors.append((rc, F.last_error()))
+    threads = [threading.Thread(target=work, args=(jobs[i::2],)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors[0]
+    for w, x, y, _ in jobs:
+        alone = torch.zeros_like(y)
+        F.dense_forward(w, x, alone)
+        assert torch.equal(alone, y)
+
+
+FIRST_IN_A_CAPTURE = """
+import torch
+from bit_scaffold_quantized_b200 import dfssm as F
+d = dict(device="cuda", dtype=torch.float16)
+x, B, C, dt = torch.randn(300, 128, **d), torch.randn(300, 64, **d), torch.randn(300, 64, **d), torch.randn(300, 2, **d)
+w, wn, wd = torch.randn(128, 4, **d), torch.ones(128, **d), torch.randn(128, 128, **d)
+par = [torch.zeros(2, device="cuda") for _ in range(3)]
+start = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+conv, ssm = torch.zeros(2, 3, 128, device="cuda"), torch.zeros(2, 2, 64, 64, device="cuda")
+y = [torch.zeros(300, 128, **d) for _ in range(6)]
+ws = F.scan_workspace(x, ssm, 2)
+
+def run():
+    F.conv_prompt(x, w, None, conv, y[0], start)
+    F.scan_prompt(y[0], dt, B, C, *par, ssm, y[1], start, ws)
+    F.gated_norm(y[1], x, wn, y[2])
+    F.dense_forward(wd, y[2], y[3])
+    F.conv_token(y[3][:2], w, None, conv, y[4][:2])
+    F.scan_token(y[4][:2], dt[:2], B[:2], C[:2], *par, ssm, y[5][:2])
+    F.dense_forward(wd, y[5][:2], y[4][2:4])
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+got = [v.clone() for v in (*y, conv, ssm)]
+for v in (*y, conv, ssm):
+    v.zero_()
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (*y, conv, ssm)))
+print("the same bits")
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "the same bits" in r.stdout, r.stdout + r.stderr
