@@ -403,7 +403,16 @@ DFSSM_API int dfssm_df_decode(const uint32_t* cells, const float* lo, const floa
  * the same slot, or when its start or end breaks the rule above.  status (device uint32,
  * may be NULL) then gets a bit or-ed in, never cleared: 1 slot >= n_slots or < -1, 2 the
  * same slot twice, 4 a bad start (64: see the scan).  Output rows of no sequence stay as
- * they were. */
+ * they were.  Where starts break the rule nothing outside the buffers is touched; what the
+ * rows of the other sequences then hold is not specified.  Limits: n_seqs <= 2^24, n_rows
+ * <= 2^30.
+ *
+ * NaN and infinity in an input reach what the formulas make of them (no number, where a
+ * formula gives either NaN or infinity) and nothing else: no earlier row, no other
+ * sequence, and not the rows and slots of those that are left out.
+ *
+ * A call may be captured, also as the first of a process, and run beside others on other
+ * streams if they share neither states nor workspace. */
 typedef struct dfssm_rows {
   void* data;
   int64_t stride;
@@ -445,8 +454,12 @@ DFSSM_API int dfssm_conv_token(int channels, int d_conv, int silu, const dfssm_r
  * as well (as the conv).  Limits: headdim a multiple of 16 and <= 128, d_state a multiple
  * of 4 and <= 256, nheads a multiple of ngroups.  The token form is one launch and needs
  * no workspace; the prompt form takes dfssm_scan_workspace_bytes bytes, not
- * initialised, not shared by calls that may overlap.  A wait inside the prompt form that
- * gives up (never seen) sets status bit 64; the outputs are then invalid. */
+ * initialised, not shared by calls that may overlap (the query and the call with the
+ * tensors' device current).  It is one to four launches.  fp16 rows of heads of 64 with 64 or
+ * 128 states, the heads of a group in pairs and the rows 16-byte aligned take tcgen05;
+ * other heads of up to 64 with up to 128 states take mma.sync, larger ones FMAs.  A wait
+ * inside the prompt form that gives up (never seen) sets status bit 64; the outputs are
+ * then invalid. */
 typedef struct dfssm_scan {
   int32_t nheads, headdim, d_state, ngroups;
   int32_t state_dtype;      /* DFSSM_DTYPE_F32 or DFSSM_DTYPE_F16 */

@@ -41,7 +41,7 @@ def test_conv_refusals(token):
     fn = L.dfssm_conv_token if token else L.dfssm_conv_prompt
     good = seqs(n=8, start=0) if token else seqs()
 
-    def call(c=64, w=4, x=rows(), wt=FAKE, b=FAKE, q=good, st=FAKE, y=rows()):
+    def call(c=64, w=4, x=rows(), wt=FAKE, b=FAKE, q=good, st=FAKE, y=rows(ptr=2 * FAKE)):
         return fn(c, w, 1, x, wt, b, q, st, y, None)
     expect(INV, call(c=0), "channels")
     expect(SHAPE, call(w=1), "d_conv")
@@ -52,6 +52,7 @@ def test_conv_refusals(token):
     expect(INV, call(x=rows(stride=63)), "stride")
     expect(INV, call(x=rows(stride=-64)), "stride")
     expect(MIS, call(x=rows(ptr=FAKE + 2)), "aligned")
+    expect(INV, call(y=rows(ptr=FAKE)), "y may not")
     expect(INV, call(wt=0), "w is NULL")
     expect(MIS, call(wt=FAKE + 2), "w is not")
     expect(MIS, call(b=FAKE + 8), "b is not")
@@ -75,7 +76,7 @@ def test_scan_refusals(token):
     L = F.lib()
     good = seqs(n=8, start=0) if token else seqs()
 
-    def call(s=scan(), x=rows(), dt=rows(), B=rows(), Cm=rows(), q=good, st=FAKE, y=rows(), ws=FAKE, n=1 << 30):
+    def call(s=scan(), x=rows(), dt=rows(), B=rows(), Cm=rows(), q=good, st=FAKE, y=rows(ptr=2 * FAKE), ws=FAKE, n=1 << 30):
         if token:
             return L.dfssm_scan_token(s, x, dt, B, Cm, q, st, y, None)
         return L.dfssm_scan_prompt(s, x, dt, B, Cm, q, st, y, ws, n, None)
@@ -94,6 +95,8 @@ def test_scan_refusals(token):
     expect(INV, call(dt=rows(stride=7)), "stride")
     expect(INV, call(B=rows(dtype=F.DTYPE_F16)), "one dtype")
     expect(MIS, call(Cm=rows(ptr=FAKE + 2)), "aligned")
+    for k in ("x", "dt", "B", "Cm"):
+        expect(INV, call(**{k: rows(ptr=2 * FAKE)}), "y may not")
     expect(MIS, call(st=FAKE + 8), "state")
     if token:
         expect(INV, call(st=0), "state is NULL")
@@ -145,6 +148,7 @@ def test_norm_and_dense_refusals():
     expect(INV, dense(x=rows(dtype=F.DTYPE_F16, stride=63)), "x: stride")
     expect(INV, dense(r=rows(ptr=2 * FAKE, dtype=F.DTYPE_F16)), "shares")
     expect(INV, dense(r=rows(ptr=0)), "residual is NULL")
+    expect(INV, dense(y=rows()), "y may not")
     expect(MIS, dense(st=FAKE + 2), "status")
     assert dense(n=0) == 0
 
