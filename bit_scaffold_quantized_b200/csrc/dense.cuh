@@ -4,6 +4,7 @@
 //                 128 tile of weight rows against N = 16 .. 256 rows of x (so that a thread,
 //                 which owns a TMEM lane, owns a weight row, and a warp's stores of one x
 //                 row are 32 consecutive values);
+//   k_dense_few   up to 32 rows of x: weights straight into mma.sync fragments;
 //   k_dense_any   rows that TMA cannot address (cols not a multiple of 8, or rows of x not
 //                 16-byte aligned).
 #pragma once
@@ -103,7 +104,8 @@ __global__ void __launch_bounds__(256) k_dense_any(DenseArgs a) {
 // 8 t .. 8 t + 7 of rows g and g + 8 in one 16-byte load each and the same columns of x row g of
 // every octet; the columns of a K = 16 product may come in any order if both sides use
 // the same, and product j takes columns 8 t + 4 j .. + 3.  At most eight products make a chain (see
-// k_dense_tc); the warps' totals meet in shared memory.
+// k_dense_tc); the warps' totals meet in shared memory.  8512 x 2048 weights, one row: 6.9 us,
+// 5.0 TB/s of weights; bound by the start of a call and the latency of its loads.
 
 __host__ __device__ constexpr size_t df_smem_bytes(int nt, int warps) {
   return size_t(4) * warps * 8 * nt * (16 + 4);
@@ -236,6 +238,9 @@ DFSSM_DEV void mbar_arrive_at(uint32_t bar) {
 // chain; the tile ends in stores alone, and the next one's MMAs run on under them.
 // K split (gridDim.z = ks pairs of one cluster): each pair sums its share of K and sends
 // (st.async) column c to pair c / (n / ks), which adds the ks sums and finishes them.
+// 4096 rows of x, 2048 x 4096 weights, fp32 residual and result: 76 us, 0.90 PFLOP/s.  With the
+// loads alone it takes 47 us, with the MMAs alone 57; what is left is the drain of the
+// accumulators (128 lanes x n columns each kDtChain stages) beside them.
 template <typename TY, typename TR>
 __global__ void __launch_bounds__(kDtThreads, 1)
     k_dense_tc(DenseArgs a, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x) {

@@ -144,9 +144,12 @@ int check_scan(const dfssm_scan* s) {
   return DFSSM_OK;
 }
 
-// Whether the prompt form runs on the tensor cores (k_scan_tc): fp16 rows of heads of 64
-// with 64 or 128 states, heads in pairs of one group.  (The rows' alignment decides at the
-// call: the workspace is large enough for either.)
+// Whether the prompt form runs on tcgen05 (k_scan_tc): fp16 rows of heads of 64 with 64 or
+// 128 states, heads in pairs of one group.  (The rows' alignment decides at the call: the
+// workspace is large enough for either.)  k_scan_tc / k_scan_mma on fp16 rows of 64 heads, us: one
+// prompt of 64 rows 16.8 / 14.1, of 256 22 / 41, of 1000 41 / 119, of 8192 167 / 881; 16 prompts of 32
+// 61 / 93.  What the shortest would gain is left: by the number of rows, a
+// short prompt's bits would depend on what it is packed with.
 enum ScanPath { kScanSimt, kScanMma, kScanTc };
 
 bool scan_tc_shape(const dfssm_scan* s, int dtype) {
@@ -165,7 +168,8 @@ struct ScanPlan {
   size_t decay_at, rec_at, big_at, bytes;
 };
 
-// Heads of up to 64 with up to 128 states run on mma.sync otherwise, larger ones on FMAs.
+// Heads of up to 64 with up to 128 states run on mma.sync otherwise (1000 rows of 64 heads in
+// fp32 126 us, on FMAs 318), larger ones, which it does not hold, on FMAs.
 ScanPath scan_other_path(const dfssm_scan* s) { return s->headdim <= kSmP && s->d_state <= 128 ? kScanMma : kScanSimt; }
 
 ScanPlan scan_plan(const dfssm_scan* s, ScanPath path, int n_seqs, int n_rows) {
@@ -236,9 +240,10 @@ ScanArgs scan_args(const dfssm_scan* s, const dfssm_rows* x, const dfssm_rows* d
 
 template <typename TX, typename TY, typename TS>
 int scan_token_launch(const ScanArgs& a, cudaStream_t st) {
-  // one pass per block while there are few blocks (latency counts), else about 128 bytes of
-  // state per thread
-  const bool few = (long long)a.q.n_seqs * a.H * a.P <= 16LL * 4 * 4 * sm_count();
+  // one pass per block while that makes about as many blocks as are resident at once, else
+  // about 128 bytes of state per thread.  One pass / several, us, heads 64 x 64 x 128 in fp32: one
+  // sequence 3.4 / 4.2, two 4.1 / 4.7, four 6.9 / 6.5, 8 11.5 / 10.1, 32 38 / 27.
+  const bool few = (long long)a.q.n_seqs * a.H * a.P <= 64LL * sm_count();
   auto go = [&](auto v, auto lanes, auto nj) {
     constexpr int V = decltype(v)::value, L = decltype(lanes)::value, NJ = decltype(nj)::value;
     constexpr int PASSES = L == 16 ? 8 / NJ : 4, ROWS = kTokThreads / L;
@@ -356,8 +361,11 @@ int norm_launch(const NormArgs& a, bool vec, cudaStream_t st) {
     return int(DFSSM_OK);
   };
   if (vec) {
+    // A warp per part once that gives every SM a block, else a block per part.  Warp / block,
+    // us: 64 parts of 1024 3.7 / 1.9, 1024 parts of 512 2.7 / 2.7 and of 1024 3.9 / 3.3, 2048
+    // parts 3.1 / 4.1 and 4.5 / 4.7, 8192 parts 7.1 / 10.8 and 12.5 / 14.1.
     if (gs <= 256) return go(k_gated_norm<TY, TZ, TO, 8, 32, 1>, 32);
-    if (gs <= 1024) return go(k_gated_norm<TY, TZ, TO, 8, 32, 4>, 32);
+    if (gs <= 1024 && a.parts > 8LL * sm_count()) return go(k_gated_norm<TY, TZ, TO, 8, 32, 4>, 32);
     if (gs <= 2048) return go(k_gated_norm<TY, TZ, TO, 8, 256, 1>, 256);
     if (gs <= 4096) return go(k_gated_norm<TY, TZ, TO, 8, 256, 2>, 256);
     if (gs <= 8192) return go(k_gated_norm<TY, TZ, TO, 8, 256, 4>, 256);

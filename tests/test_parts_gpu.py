@@ -439,6 +439,18 @@ def test_gated_norm(rows, cols, groups, yt, zt, ot, pads):
     check("out", host(out), want, norm_tol(want, cols // groups, ot))
 
 
+@pytest.mark.parametrize("rows,cols,groups", [(1500, 520, 1), (700, 2048, 2), (1300, 1024, 1)])
+def test_gated_norm_many_rows(rows, cols, groups):
+    """Enough parts for a warp each."""
+    rng = np.random.default_rng(43)
+    y, z = rng.normal(size=(rows, cols)).astype(np.float32), rng.normal(size=(rows, cols)).astype(np.float16)
+    w = rng.normal(size=cols, loc=1.0, scale=0.1).astype(np.float16)
+    want = PO.gated_norm(y, z, w, groups)
+    out = torch.full((rows, cols), MARK, dtype=F16, device=DEV)
+    F.gated_norm(dev(y), dev(z), dev(w), out, groups)
+    check("out", host(out), want, norm_tol(want, cols // groups, F16))
+
+
 def test_gated_norm_in_place_and_extremes():
     rng = np.random.default_rng(42)
     for cols in (512, 4096, 9000):
