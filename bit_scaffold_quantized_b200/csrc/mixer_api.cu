@@ -98,6 +98,7 @@ int conv_launch(ConvArgs a, bool token, cudaStream_t st) {
 int conv(int channels, int d_conv, int silu, const dfssm_rows* x, const uint16_t* w, const uint16_t* b,
          const dfssm_seqs* seqs, float* state, const dfssm_rows* y, bool token, void* stream) {
   REQUIRE(channels > 0, DFSSM_ERR_INVALID_ARG, "channels (%d) must be positive", channels);
+  REQUIRE(channels <= 1 << 28, DFSSM_ERR_UNSUPPORTED_SHAPE, "channels (%d) > 2^28", channels);
   REQUIRE(d_conv >= 2 && d_conv <= 4, DFSSM_ERR_UNSUPPORTED_SHAPE, "d_conv (%d) must be 2, 3 or 4", d_conv);
   int rc;
   if ((rc = check_rows(x, "x", channels)) || (rc = check_rows(y, "y", channels))) return rc;
@@ -596,6 +597,7 @@ int dfssm_gated_norm(int rows, int cols, int ngroups, const dfssm_rows* y, const
                      const dfssm_rows* out, void* stream) {
   REQUIRE(rows >= 0 && cols > 0 && ngroups > 0, DFSSM_ERR_INVALID_ARG, "rows (%d), cols (%d) or ngroups (%d) out of range",
           rows, cols, ngroups);
+  REQUIRE(cols <= 1 << 30, DFSSM_ERR_UNSUPPORTED_SHAPE, "cols (%d) > 2^30", cols);
   REQUIRE(cols % ngroups == 0, DFSSM_ERR_UNSUPPORTED_SHAPE, "cols (%d) is not a multiple of ngroups (%d)", cols, ngroups);
   int rc;
   if ((rc = check_rows(y, "y", cols)) || (rc = check_rows(out, "out", cols))) return rc;
@@ -627,6 +629,8 @@ int dfssm_dense_forward(int rows, int cols, int batch, const uint16_t* w, const 
                         void* stream) {
   REQUIRE(rows > 0 && cols > 0 && batch >= 0, DFSSM_ERR_INVALID_ARG, "rows (%d), cols (%d) or batch (%d) out of range", rows,
           cols, batch);
+  REQUIRE(rows <= 1 << 30 && cols <= 1 << 30 && batch <= 1 << 30, DFSSM_ERR_UNSUPPORTED_SHAPE,
+          "rows (%d), cols (%d) or batch (%d) > 2^30", rows, cols, batch);
   REQUIRE_PTR(w);
   REQUIRE(aligned16(b), DFSSM_ERR_MISALIGNED, "b is not 16-byte aligned");
   int rc;

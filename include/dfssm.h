@@ -405,7 +405,7 @@ DFSSM_API int dfssm_df_decode(const uint32_t* cells, const float* lo, const floa
  * same slot twice, 4 a bad start (64: see the scan).  Output rows of no sequence stay as
  * they were.  Where starts break the rule nothing outside the buffers is touched; what the
  * rows of the other sequences then hold is not specified.  Limits: n_seqs <= 2^24, n_rows
- * <= 2^30.
+ * <= 2^30, channels <= 2^28, the norm's cols and the projection's sizes <= 2^30.
  *
  * NaN and infinity in an input reach what the formulas make of them (no number, where a
  * formula gives either NaN or infinity) and nothing else: no earlier row, no other

@@ -44,6 +44,7 @@ def test_conv_refusals(token):
     def call(c=64, w=4, x=rows(), wt=FAKE, b=FAKE, q=good, st=FAKE, y=rows(ptr=2 * FAKE)):
         return fn(c, w, 1, x, wt, b, q, st, y, None)
     expect(INV, call(c=0), "channels")
+    expect(SHAPE, call(c=(1 << 28) + 4, x=rows(stride=1 << 30)), "channels")
     expect(SHAPE, call(w=1), "d_conv")
     expect(SHAPE, call(w=5), "d_conv")
     expect(INV, call(x=NULL), "x is NULL")
@@ -129,6 +130,7 @@ def test_norm_and_dense_refusals():
     expect(INV, norm(r=-1), "rows")
     expect(INV, norm(g=0), "ngroups")
     expect(SHAPE, norm(g=3), "ngroups")
+    expect(SHAPE, norm(c=(1 << 30) + 8), "cols")
     expect(INV, norm(y=NULL), "y is NULL")
     expect(INV, norm(w=0), "w is NULL")
     expect(INV, norm(z=rows(stride=511)), "z: stride")
@@ -141,6 +143,8 @@ def test_norm_and_dense_refusals():
         return L.dfssm_dense_forward(o, k, n, w, b, 0, x, r, y, st, None)
     expect(INV, dense(o=0), "rows")
     expect(INV, dense(n=-1), "batch")
+    for k in "okn":
+        expect(SHAPE, dense(**{k: (1 << 30) + 8}), "2^30")
     expect(INV, dense(w=0), "w is NULL")
     expect(MIS, dense(w=FAKE + 2), "w is not")
     expect(MIS, dense(b=FAKE + 2), "b is not")
