@@ -776,8 +776,9 @@ constexpr int kNormThreads = 256;
 
 // THREADS threads (a warp or the block) per part of gs = cols / groups values, held in
 // registers: NV pieces of VEC per thread, y and z read once.  Bound by memory: 8192 rows of 4096
-// in fp16 with a gate take 39 us, 5.1 TB/s of the 6.6 of a copy; 64 rows in fp32 3.6 us, the
-// launch and one round of loads.
+// in fp16 with a gate take 38 us, 5.3 TB/s of the 6.6 of a copy (37 registers, six blocks an SM;
+// with every load before the first use it holds more and takes 47); 64 rows in fp32 3.6 us,
+// the launch and one round of loads.
 template <typename TY, typename TZ, typename TO, int VEC, int THREADS, int NV>
 __global__ void __launch_bounds__(kNormThreads) k_gated_norm(NormArgs a) {
   pdl_wait();
@@ -820,8 +821,10 @@ __global__ void __launch_bounds__(kNormThreads) k_gated_norm(NormArgs a) {
   for (int k = 0; k < NV; ++k) {
     const int c = (t + THREADS * k) * VEC;
     if (c < gs) {
+      float w[VEC];
+      ldv<VEC>(reinterpret_cast<const __half*>(a.w) + c0 + c, w);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[k][i] = v[k][i] * rs * h2f(a.w[c0 + c + i]);
+      for (int i = 0; i < VEC; ++i) v[k][i] = v[k][i] * rs * w[i];
       stv<VEC>(op + c, v[k]);
     }
   }
