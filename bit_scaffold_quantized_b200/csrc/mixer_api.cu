@@ -170,7 +170,7 @@ struct ScanPlan {
 };
 
 // Heads of up to 64 with up to 128 states run on mma.sync otherwise (1000 rows of 64 heads in
-// fp32 126 us, on FMAs 318), larger ones, which it does not hold, on FMAs.
+// fp32 129 us, on FMAs 318), larger ones, which it does not hold, on FMAs.
 ScanPath scan_other_path(const dfssm_scan* s) { return s->headdim <= kSmP && s->d_state <= 128 ? kScanMma : kScanSimt; }
 
 ScanPlan scan_plan(const dfssm_scan* s, ScanPath path, int n_seqs, int n_rows) {

@@ -16,7 +16,7 @@ namespace dfssm {
 // 16 rows t x a quarter of the columns; S and H: warp = 16 rows p x a quarter of the columns n,
 // H in registers (fp32) throughout.  The next chunk's rows are on
 // their way in registers meanwhile.
-// 1000 rows of 64 heads of 64 with 128 states in fp32 take 126 us, the states between
+// 1000 rows of 64 heads of 64 with 128 states in fp32 take 129 us, the states between
 // segments and the join included (on FMAs, as k_scan_prompt: 318; eight warps: 130), 18 times
 // what their bytes take.  It is bound by the latency of its phases, one block an SM: of the 15.8
 // thousand cycles of a chunk the conversion to pieces takes 2-3, CB 2.5, S 1.9, the running
